@@ -12,6 +12,9 @@
  *                                writes packed codes, fp16 scales and packed zero points.
  *   4. gptq_pack_int / gptq_dequant   packing of b-bit codes; W_hat = s * (q - z).
  *   5. gptq_dequant_gemm         Y = X W_hat^T straight from the packed arrays.
+ *      gptq_dequant_gemv         the same for a few tokens (decoding), every packed layout.
+ *      gptq_dequant_gemm_e4m3    the same for 8-bit activations, which
+ *      gptq_rms_norm_e4m3 and gptq_quantize_e4m3 write.
  *
  * Activation ordering (desc_act) visits the columns in another order:
  * gptq_act_sum_accumulate (beside stage 1) and gptq_act_order rank the columns,
@@ -65,7 +68,11 @@ typedef enum {
     GPTQ_ERR_WORKSPACE = 7      /* workspace missing or smaller than the query returned */
 } gptq_status;
 
-typedef enum { GPTQ_BF16 = 0, GPTQ_F32 = 1 } gptq_dtype;
+typedef enum {
+    GPTQ_BF16 = 0,
+    GPTQ_F32 = 1,
+    GPTQ_E4M3 = 2   /* 8-bit floats (4 exponent, 3 fraction bits, largest 448), one fp32 scale per row */
+} gptq_dtype;
 
 /* Quantization settings (tutorial "代码示例" BaseQuantizeConfig: bits, group_size,
  * desc_act; group-size article: sym).
@@ -253,6 +260,55 @@ gptq_status gptq_dequant_g_idx(const int32_t* qweight, const uint16_t* scales, c
 gptq_status gptq_dequant_gemm(const void* X, int64_t M, const int32_t* qweight, const uint16_t* scales,
                               const int32_t* qzeros, int64_t d_out, int64_t d_in, const gptq_config* cfg, float* Y,
                               void* stream);
+
+/* ------------------------------------------------------------------ product of a few tokens
+ * Y[m, n] = x_scale[m] * sum_k X[m, k] * W_hat[n, k] for M <= GPTQ_GEMV_MAX_M rows of X, the
+ * decoding form of gptq_dequant_gemm, for every layout that gptq_quantize_layer and
+ * gptq_quantize_layer_act_order write: bits 2, 3, 4 or 8, any group_size, symmetric or not.
+ *   X        device [M, d_in] row-major, bf16, or e4m3 bytes with x_scale.
+ *   x_scale  device fp32 [M] iff X is e4m3, else NULL.
+ *   g_idx    device int32 [d_in] iff cfg->desc_act != 0, else NULL.  An entry outside
+ *            [0, n_groups) is reported by the next gptq_sync_status() (GPTQ_ERR_INVALID_ARG).
+ *   Y        device [M, d_out] row-major, bf16 or fp32 (yt), written in full; apart from the inputs.
+ * Sums are fp32 in a fixed order (the same bits on every run); no rounded copy of W_hat is made,
+ * and a bf16 Y is rounded once.  A non-finite X makes its own row of Y non-finite and no other.
+ * Requires 1 <= M <= GPTQ_GEMV_MAX_M, d_in % 8 == 0, 1 <= d_out; X aligned to 8 elements,
+ * qweight, scales and qzeros to 16 bytes.  No workspace, nothing is allocated. */
+#define GPTQ_GEMV_MAX_M 64
+gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale, int64_t M, const int32_t* qweight,
+                              const uint16_t* scales, const int32_t* qzeros, const int32_t* g_idx, int64_t d_out,
+                              int64_t d_in, const gptq_config* cfg, void* Y, gptq_dtype yt, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit activations
+ * gptq_rms_norm_e4m3, for each of the M rows:
+ *   h = X + residual (X alone without one),  y_k = h_k weight_k / sqrt(mean_k h_k^2 + eps),
+ *   x_scale = max_k |y_k| / 448,  X8_k = e4m3(y_k / x_scale) (nearest, ties to even),
+ *   residual_out = h rounded to X's type.
+ * gptq_quantize_e4m3 does the same for y = X.
+ *   X, residual, residual_out  device [M, d_in] row-major, bf16 or fp32 (xt).  residual and
+ *            residual_out are given together or both NULL; residual_out may be residual or X.
+ *   weight   device [d_in], bf16 or fp32 (wt).
+ *   X8       device [M, d_in] e4m3 bytes;  x_scale device fp32 [M].
+ * h, the sum and the maximum are fp32: y comes from the unrounded h.  A row whose y is all zero
+ * gets x_scale 0 and zero codes.  A row with a NaN or an infinity gets a non-finite x_scale (its
+ * products are then non-finite) and leaves the others alone.  Magnitudes of h below 2^60.
+ * Requires d_in % 8 == 0, d_in <= 65536; X8 8-byte, the other arrays 16-byte aligned (x_scale 4). */
+gptq_status gptq_rms_norm_e4m3(const void* X, const void* residual, gptq_dtype xt, const void* weight, gptq_dtype wt,
+                               int64_t M, int64_t d_in, float eps, uint8_t* X8, float* x_scale, void* residual_out,
+                               void* stream);
+gptq_status gptq_quantize_e4m3(const void* X, gptq_dtype xt, int64_t M, int64_t d_in, uint8_t* X8, float* x_scale,
+                               void* stream);
+
+/* Y[m, n] = x_scale[m] * sum_k X8[m, k] * W_hat[n, k] for any number of rows: gptq_dequant_gemm on
+ * 8-bit activations.  X8 and x_scale as written by the two calls above, Y bf16 or fp32 (yt).
+ * q - z of 2, 3 and 4 bits is exact in e4m3, so each group's products are exact; they are summed
+ * in fp32, scaled by the group's fp16 scales and summed in fp32 in a fixed order.
+ * Requires bits 2, 3 or 4, group_size -1 or 32, 64, 128 dividing d_in, desc_act 0
+ * (GPTQ_ERR_UNSUPPORTED otherwise), d_in % 32 == 0, d_out % 8 == 0, X8, Y and the packed arrays
+ * 16-byte aligned.  No workspace. */
+gptq_status gptq_dequant_gemm_e4m3(const uint8_t* X8, const float* x_scale, int64_t M, const int32_t* qweight,
+                                   const uint16_t* scales, const int32_t* qzeros, int64_t d_out, int64_t d_in,
+                                   const gptq_config* cfg, void* Y, gptq_dtype yt, void* stream);
 
 /* ------------------------------------------------------------------ layer output error
  * E = ||(W - W_hat) X^T||_F^2 (tutorial "阶段一": the squared error of the layer's outputs

@@ -19,6 +19,8 @@
 #include "pack.cuh"
 #include "colloop_host.cuh"
 #include "dqgemm.cuh"
+#include "gemv.cuh"
+#include "rows_e4m3.cuh"
 #include "gptq2d.cuh"
 #include "loss.cuh"
 
@@ -234,6 +236,7 @@ static gptq_status cuda_fail(cudaError_t e, const char* where) {
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 static gptq_status check_config(const gptq_config* cfg) {
     if (!cfg) return fail(GPTQ_ERR_INVALID_ARG, "cfg is NULL");
@@ -623,6 +626,140 @@ gptq_status gptq_dequant_gemm(const void* X, int64_t M, const int32_t* qweight, 
         default: e = dq_gemm_run<8>(X, M, qweight, sc, qzeros, d_out, d_in, g, Y, st); break;
     }
     if (e != cudaSuccess) return cuda_fail(e, "dequant_gemm");
+    return GPTQ_OK;
+}
+
+// The arguments that every product with packed weights shares.
+static gptq_status check_product(const void* X, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                                 int64_t d_out, int64_t d_in, const gptq_config* cfg, const void* Y, gptq_dtype yt) {
+    gptq_status cs = check_config(cfg);
+    if (cs != GPTQ_OK) return cs;
+    if (!X || !qweight || !scales || !Y) return fail(GPTQ_ERR_INVALID_ARG, "X, qweight, scales and Y must be non-NULL");
+    if (cfg->sym ? (qzeros != nullptr) : (qzeros == nullptr))
+        return fail(GPTQ_ERR_INVALID_ARG, "qzeros must be given iff asymmetric");
+    if (d_in < 8 || d_in > 65536 || d_in % 8) return fail(GPTQ_ERR_INVALID_ARG, "d_in must be a multiple of 8 in [8, 65536]");
+    if (d_out < 1 || d_out > (1ll << 30)) return fail(GPTQ_ERR_INVALID_ARG, "d_out out of range (%lld)", (long long)d_out);
+    if (yt != GPTQ_BF16 && yt != GPTQ_F32) return fail(GPTQ_ERR_INVALID_ARG, "Y must be bf16 or fp32 (dtype %d)", (int)yt);
+    if (!aligned16(qweight) || !aligned16(scales) || !aligned16(qzeros))
+        return fail(GPTQ_ERR_INVALID_ARG, "qweight, scales and qzeros must be 16-byte aligned");
+    return GPTQ_OK;
+}
+
+gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale, int64_t M, const int32_t* qweight,
+                              const uint16_t* scales, const int32_t* qzeros, const int32_t* g_idx, int64_t d_out,
+                              int64_t d_in, const gptq_config* cfg, void* Y, gptq_dtype yt, void* stream) {
+    gptq_status cs = check_product(X, qweight, scales, qzeros, d_out, d_in, cfg, Y, yt);
+    if (cs != GPTQ_OK) return cs;
+    if (xt != GPTQ_BF16 && xt != GPTQ_E4M3) return fail(GPTQ_ERR_INVALID_ARG, "X must be bf16 or e4m3 (dtype %d)", (int)xt);
+    if ((xt == GPTQ_E4M3) != (x_scale != nullptr))
+        return fail(GPTQ_ERR_INVALID_ARG, "x_scale must be given iff X is e4m3");
+    if (M < 1 || M > GPTQ_GEMV_MAX_M)
+        return fail(GPTQ_ERR_INVALID_ARG, "M must be in [1, %d] (got %lld)", GPTQ_GEMV_MAX_M, (long long)M);
+    if ((cfg->desc_act != 0) != (g_idx != nullptr))
+        return fail(GPTQ_ERR_INVALID_ARG, "g_idx must be given iff desc_act is not 0");
+    if (misaligned(X, xt == GPTQ_BF16 ? 16 : 8) || misaligned(x_scale, 4) || misaligned(g_idx, 4) ||
+        misaligned(Y, yt == GPTQ_BF16 ? 2 : 4))
+        return fail(GPTQ_ERR_INVALID_ARG, "X must be aligned to 8 elements, x_scale, g_idx and Y to their own");
+    gq::GemvArgs p{};
+    p.X = X;
+    p.x_scale = x_scale;
+    p.qweight = qweight;
+    p.scales = reinterpret_cast<const __half*>(scales);
+    p.qzeros = qzeros;
+    p.g_idx = g_idx;
+    p.Y = Y;
+    p.y_bf16 = yt == GPTQ_BF16;
+    p.M = (int)M;
+    p.N = d_out;
+    p.K = d_in;
+    p.g = cfg->group_size < 0 ? (int)d_in : cfg->group_size;
+    p.ng = (int)((d_in + p.g - 1) / p.g);
+    p.bits = cfg->bits;
+    cudaError_t e = gemv_run(p, xt == GPTQ_E4M3, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "dequant_gemv");
+    return GPTQ_OK;
+}
+
+static gptq_status check_rows(const void* X, gptq_dtype xt, int64_t M, int64_t d_in, const uint8_t* X8,
+                              const float* x_scale) {
+    if (!X || !X8 || !x_scale) return fail(GPTQ_ERR_INVALID_ARG, "X, X8 and x_scale must be non-NULL");
+    if (xt != GPTQ_BF16 && xt != GPTQ_F32) return fail(GPTQ_ERR_INVALID_ARG, "X must be bf16 or fp32 (dtype %d)", (int)xt);
+    if (M < 1 || M > (1ll << 30)) return fail(GPTQ_ERR_INVALID_ARG, "M out of range (%lld)", (long long)M);
+    if (d_in < 8 || d_in > 65536 || d_in % 8) return fail(GPTQ_ERR_INVALID_ARG, "d_in must be a multiple of 8 in [8, 65536]");
+    if (!aligned16(X) || misaligned(X8, 8) || misaligned(x_scale, 4))
+        return fail(GPTQ_ERR_INVALID_ARG, "X must be 16-byte aligned, X8 8-byte, x_scale 4-byte");
+    return GPTQ_OK;
+}
+
+gptq_status gptq_rms_norm_e4m3(const void* X, const void* residual, gptq_dtype xt, const void* weight, gptq_dtype wt,
+                               int64_t M, int64_t d_in, float eps, uint8_t* X8, float* x_scale, void* residual_out,
+                               void* stream) {
+    gptq_status cs = check_rows(X, xt, M, d_in, X8, x_scale);
+    if (cs != GPTQ_OK) return cs;
+    if (!weight) return fail(GPTQ_ERR_INVALID_ARG, "weight must be non-NULL");
+    if (wt != GPTQ_BF16 && wt != GPTQ_F32) return fail(GPTQ_ERR_INVALID_ARG, "weight must be bf16 or fp32 (dtype %d)", (int)wt);
+    if ((residual == nullptr) != (residual_out == nullptr))
+        return fail(GPTQ_ERR_INVALID_ARG, "residual and residual_out must be given together");
+    if (!aligned16(weight) || !aligned16(residual) || !aligned16(residual_out))
+        return fail(GPTQ_ERR_INVALID_ARG, "weight, residual and residual_out must be 16-byte aligned");
+    if (!(eps >= 0.f) || eps > 1e30f) return fail(GPTQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    const gq::RowsArgs p{X, residual, weight, X8, x_scale, residual_out, d_in, eps};
+    cudaStream_t st = (cudaStream_t)stream;
+    const char* name = "rms_norm_e4m3";
+    cudaError_t e;
+    if (xt == GPTQ_BF16)
+        e = wt == GPTQ_BF16 ? rows_e4m3_run<__nv_bfloat16, __nv_bfloat16, true>(p, M, name, st)
+                            : rows_e4m3_run<__nv_bfloat16, float, true>(p, M, name, st);
+    else
+        e = wt == GPTQ_BF16 ? rows_e4m3_run<float, __nv_bfloat16, true>(p, M, name, st)
+                            : rows_e4m3_run<float, float, true>(p, M, name, st);
+    if (e != cudaSuccess) return cuda_fail(e, "rms_norm_e4m3");
+    return GPTQ_OK;
+}
+
+gptq_status gptq_quantize_e4m3(const void* X, gptq_dtype xt, int64_t M, int64_t d_in, uint8_t* X8, float* x_scale,
+                               void* stream) {
+    gptq_status cs = check_rows(X, xt, M, d_in, X8, x_scale);
+    if (cs != GPTQ_OK) return cs;
+    const gq::RowsArgs p{X, nullptr, nullptr, X8, x_scale, nullptr, d_in, 0.f};
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = xt == GPTQ_BF16 ? rows_e4m3_run<__nv_bfloat16, float, false>(p, M, "quantize_e4m3", st)
+                                    : rows_e4m3_run<float, float, false>(p, M, "quantize_e4m3", st);
+    if (e != cudaSuccess) return cuda_fail(e, "quantize_e4m3");
+    return GPTQ_OK;
+}
+
+gptq_status gptq_dequant_gemm_e4m3(const uint8_t* X8, const float* x_scale, int64_t M, const int32_t* qweight,
+                                   const uint16_t* scales, const int32_t* qzeros, int64_t d_out, int64_t d_in,
+                                   const gptq_config* cfg, void* Y, gptq_dtype yt, void* stream) {
+    gptq_status cs = check_product(X8, qweight, scales, qzeros, d_out, d_in, cfg, Y, yt);
+    if (cs != GPTQ_OK) return cs;
+    if (!x_scale) return fail(GPTQ_ERR_INVALID_ARG, "x_scale must be non-NULL");
+    if (M < 1 || M > (1ll << 30)) return fail(GPTQ_ERR_INVALID_ARG, "M out of range (%lld)", (long long)M);
+    if (d_in % 32 || d_out % 8) return fail(GPTQ_ERR_INVALID_ARG, "d_in must be a multiple of 32 and d_out of 8");
+    if (!aligned16(X8) || !aligned16(Y) || misaligned(x_scale, 4))
+        return fail(GPTQ_ERR_INVALID_ARG, "X8 and Y must be 16-byte aligned, x_scale 4-byte");
+    if (cfg->bits == 8) return fail(GPTQ_ERR_UNSUPPORTED, "dequant_gemm_e4m3: 8-bit q - z is not an e4m3 value");
+    const int g = cfg->group_size;
+    if (!(g == -1 || (g >= 32 && d_in % g == 0)))
+        return fail(GPTQ_ERR_UNSUPPORTED, "dequant_gemm_e4m3: group_size must be -1, 32, 64 or 128 and divide d_in");
+    if (cfg->desc_act) return fail(GPTQ_ERR_UNSUPPORTED, "dequant_gemm_e4m3: no per-column group index (desc_act)");
+    gq::GemvArgs p{};
+    p.X = X8;
+    p.x_scale = x_scale;
+    p.qweight = qweight;
+    p.scales = reinterpret_cast<const __half*>(scales);
+    p.qzeros = qzeros;
+    p.Y = Y;
+    p.y_bf16 = yt == GPTQ_BF16;
+    p.M = (int)M;
+    p.N = d_out;
+    p.K = d_in;
+    p.g = g < 0 ? (int)d_in : g;
+    p.ng = (int)(d_in / p.g);
+    p.bits = cfg->bits;
+    cudaError_t e = gemv_run(p, true, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "dequant_gemm_e4m3");
     return GPTQ_OK;
 }
 

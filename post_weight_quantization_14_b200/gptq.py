@@ -30,6 +30,9 @@ GPTQ_ERR_WORKSPACE = 7
 
 GPTQ_BF16 = 0
 GPTQ_F32 = 1
+GPTQ_E4M3 = 2
+
+GPTQ_GEMV_MAX_M = 64   # rows of X that gptq_dequant_gemv takes
 
 
 class GptqConfig(ctypes.Structure):
@@ -79,6 +82,12 @@ _SIGS = {
                                              _vp, _vp, _vp, _sz, _vp]),
     "gptq_dequant_g_idx": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, ctypes.POINTER(GptqConfig), _vp, _vp]),
     "gptq_dequant_gemm": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, ctypes.POINTER(GptqConfig), _vp, _vp]),
+    "gptq_dequant_gemv": (_int, [_vp, _int, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, ctypes.POINTER(GptqConfig), _vp,
+                                 _int, _vp]),
+    "gptq_rms_norm_e4m3": (_int, [_vp, _vp, _int, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp]),
+    "gptq_quantize_e4m3": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp]),
+    "gptq_dequant_gemm_e4m3": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, ctypes.POINTER(GptqConfig), _vp, _int,
+                                      _vp]),
     "gptq_layer_loss_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "gptq_layer_loss": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
     "gptq_2d_workspace_bytes": (_sz, [_i64, _i64, _i64]),
@@ -341,6 +350,103 @@ def gptq_dequant_gemm(X: torch.Tensor, qweight, scales, qzeros, d_out: int, d_in
     _quant_outputs(cfg, d_out, d_in, qweight, scales, qzeros, None)
     _check(lib().gptq_dequant_gemm(_ptr(X), X.shape[0], _ptr(qweight), _ptr(scales), _ptr(qzeros), d_out, d_in,
                                    ctypes.byref(cfg), _ptr(Y), _stream(stream)))
+    return Y
+
+
+_DTYPES = {torch.bfloat16: GPTQ_BF16, torch.float32: GPTQ_F32, torch.float8_e4m3fn: GPTQ_E4M3}
+
+
+def _dtype(t: torch.Tensor, allowed: tuple, name: str) -> int:
+    if t.dtype not in allowed:
+        raise ValueError(f"{name} must be {' or '.join(str(d)[6:] for d in allowed)} (got {t.dtype})")
+    return _DTYPES[t.dtype]
+
+
+def _ptrs(*tensors: torch.Tensor | None) -> list[int | None]:
+    """Addresses of contiguous tensors that all sit on the current CUDA device."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+    return [_ptr(t) for t in tensors]
+
+
+def gptq_dequant_gemv(X: torch.Tensor, qweight, scales, qzeros, d_out: int, d_in: int, cfg: GptqConfig,
+                      Y: torch.Tensor, x_scale: torch.Tensor | None = None, g_idx: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Y = X W_hat^T for up to GPTQ_GEMV_MAX_M rows, from any packed layout.  X: bfloat16 [M, d_in], or
+    float8_e4m3fn with x_scale float32 [M]; Y: bfloat16 or float32 [M, d_out]; g_idx: int32 [d_in] iff
+    cfg.desc_act."""
+    xt = _dtype(X, (torch.bfloat16, torch.float8_e4m3fn), "X")
+    yt = _dtype(Y, (torch.bfloat16, torch.float32), "Y")
+    if X.dim() != 2:
+        raise ValueError("X must be a [M, d_in] matrix")
+    M = X.shape[0]
+    _need(X, X.dtype, (M, d_in), "X")
+    _need(Y, Y.dtype, (M, d_out), "Y")
+    _quant_outputs(cfg, d_out, d_in, qweight, scales, qzeros, None)
+    if (x_scale is not None) != (xt == GPTQ_E4M3):
+        raise ValueError("x_scale must be given iff X is float8_e4m3fn")
+    if x_scale is not None:
+        _need(x_scale, torch.float32, (M,), "x_scale")
+    if (g_idx is not None) != (cfg.desc_act != 0):
+        raise ValueError("g_idx must be given iff cfg.desc_act is not 0")
+    if g_idx is not None:
+        _need(g_idx, torch.int32, (d_in,), "g_idx")
+    x, xs, w, s, z, gi, y = _ptrs(X, x_scale, qweight, scales, qzeros, g_idx, Y)
+    _check(lib().gptq_dequant_gemv(x, xt, xs, M, w, s, z, gi, d_out, d_in, ctypes.byref(cfg), y, yt, _stream(stream)))
+    return Y
+
+
+def gptq_rms_norm_e4m3(X: torch.Tensor, weight: torch.Tensor, X8: torch.Tensor, x_scale: torch.Tensor,
+                       residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                       eps: float = 1e-6, stream=None) -> None:
+    """Root-mean-square norm of X + residual to float8_e4m3fn rows X8 with float32 scales x_scale [M];
+    residual_out receives X + residual (it may be residual or X).  X, residual: bfloat16 or float32
+    [M, d_in]; weight: bfloat16 or float32 [d_in]."""
+    xt = _dtype(X, (torch.bfloat16, torch.float32), "X")
+    wt = _dtype(weight, (torch.bfloat16, torch.float32), "weight")
+    if X.dim() != 2:
+        raise ValueError("X must be a [M, d_in] matrix")
+    M, d_in = X.shape
+    _need(weight, weight.dtype, (d_in,), "weight")
+    _need(X8, torch.float8_e4m3fn, (M, d_in), "X8")
+    _need(x_scale, torch.float32, (M,), "x_scale")
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out must be given together")
+    if residual is not None:
+        _need(residual, X.dtype, (M, d_in), "residual")
+        _need(residual_out, X.dtype, (M, d_in), "residual_out")
+    x, r, w, x8, xs, r2 = _ptrs(X, residual, weight, X8, x_scale, residual_out)
+    _check(lib().gptq_rms_norm_e4m3(x, r, xt, w, wt, M, d_in, eps, x8, xs, r2, _stream(stream)))
+
+
+def gptq_quantize_e4m3(X: torch.Tensor, X8: torch.Tensor, x_scale: torch.Tensor, stream=None) -> None:
+    """Rows of X (bfloat16 or float32 [M, d_in]) to float8_e4m3fn X8 with float32 scales x_scale [M]."""
+    xt = _dtype(X, (torch.bfloat16, torch.float32), "X")
+    if X.dim() != 2:
+        raise ValueError("X must be a [M, d_in] matrix")
+    M, d_in = X.shape
+    _need(X8, torch.float8_e4m3fn, (M, d_in), "X8")
+    _need(x_scale, torch.float32, (M,), "x_scale")
+    x, x8, xs = _ptrs(X, X8, x_scale)
+    _check(lib().gptq_quantize_e4m3(x, xt, M, d_in, x8, xs, _stream(stream)))
+
+
+def gptq_dequant_gemm_e4m3(X8: torch.Tensor, x_scale: torch.Tensor, qweight, scales, qzeros, d_out: int, d_in: int,
+                           cfg: GptqConfig, Y: torch.Tensor, stream=None) -> torch.Tensor:
+    """Y = diag(x_scale) X8 W_hat^T from the packed arrays.  X8: float8_e4m3fn [M, d_in]; x_scale: float32
+    [M]; Y: bfloat16 or float32 [M, d_out]."""
+    yt = _dtype(Y, (torch.bfloat16, torch.float32), "Y")
+    if X8.dim() != 2:
+        raise ValueError("X8 must be a [M, d_in] matrix")
+    M = X8.shape[0]
+    _need(X8, torch.float8_e4m3fn, (M, d_in), "X8")
+    _need(x_scale, torch.float32, (M,), "x_scale")
+    _need(Y, Y.dtype, (M, d_out), "Y")
+    _quant_outputs(cfg, d_out, d_in, qweight, scales, qzeros, None)
+    x, xs, w, s, z, y = _ptrs(X8, x_scale, qweight, scales, qzeros, Y)
+    _check(lib().gptq_dequant_gemm_e4m3(x, xs, M, w, s, z, d_out, d_in, ctypes.byref(cfg), y, yt, _stream(stream)))
     return Y
 
 
