@@ -3,6 +3,7 @@
 // the kernels of the included headers.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -19,6 +20,7 @@
 #include "pack.cuh"
 #include "colloop_host.cuh"
 #include "dqgemm.cuh"
+#include "dqgemm_e4m3.cuh"
 #include "gemv.cuh"
 #include "rows_e4m3.cuh"
 #include "gptq2d.cuh"
@@ -744,21 +746,22 @@ gptq_status gptq_dequant_gemm_e4m3(const uint8_t* X8, const float* x_scale, int6
     if (!(g == -1 || (g >= 32 && d_in % g == 0)))
         return fail(GPTQ_ERR_UNSUPPORTED, "dequant_gemm_e4m3: group_size must be -1, 32, 64 or 128 and divide d_in");
     if (cfg->desc_act) return fail(GPTQ_ERR_UNSUPPORTED, "dequant_gemm_e4m3: no per-column group index (desc_act)");
-    gq::GemvArgs p{};
-    p.X = X8;
-    p.x_scale = x_scale;
-    p.qweight = qweight;
+    if (M > (1ll << 30) - 256 || d_out > (1ll << 30) - 256)
+        return fail(GPTQ_ERR_INVALID_ARG, "M and d_out must be at most 2^30 - 256");
+    gq::D8Args p{};
     p.scales = reinterpret_cast<const __half*>(scales);
     p.qzeros = qzeros;
+    p.x_scale = x_scale;
     p.Y = Y;
     p.y_bf16 = yt == GPTQ_BF16;
     p.M = (int)M;
-    p.N = d_out;
-    p.K = d_in;
-    p.g = g < 0 ? (int)d_in : g;
-    p.ng = (int)(d_in / p.g);
-    p.bits = cfg->bits;
-    cudaError_t e = gemv_run(p, true, (cudaStream_t)stream);
+    p.N = (int)d_out;
+    p.K = (int)d_in;
+    p.spt = g < 0 ? 0 : 128 / g;
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = cfg->bits == 2   ? dq_gemm_e4m3_run<2>(X8, qweight, p, st)
+                    : cfg->bits == 3 ? dq_gemm_e4m3_run<3>(X8, qweight, p, st)
+                                     : dq_gemm_e4m3_run<4>(X8, qweight, p, st);
     if (e != cudaSuccess) return cuda_fail(e, "dequant_gemm_e4m3");
     return GPTQ_OK;
 }
