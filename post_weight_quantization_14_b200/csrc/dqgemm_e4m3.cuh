@@ -11,20 +11,27 @@
 // tcgen05.st, so shared memory carries only X8 (the B operand) and the packed words.  With rows
 // on the lanes, a group's scale is one register of an epilogue thread.
 //
-// A tile is 128 rows x TT tokens, K advances by 128.  One CTA per SM, 16 warps:
-//   warp 0       TMA: X8 tile (TT tokens x 128 bytes, 128-byte swizzle) and packed words
-//                (4 BITS words x 128 rows) into a ring of stages;
-//   warp 1       MMA issuer: per quantization group one accumulator segment for each half of
-//                up to 128 tokens, in a ring of three accumulators of tensor memory;
-//   warps 4-7    converters, one thread per row, a ring of four A operands of 32 columns;
+// A tile is 128 rows x TT tokens, K advances by 128.  One CTA per SM, 20 warps:
+//   warps 0-7    converters, two sets that take turns, a thread per row, a ring of four A
+//                operands of 32 columns;
 //   warps 8-15   epilogue: two warps per lane quadrant, TT / 2 tokens each, running sums in
-//                registers: y += s_g P_g, two at a time.
-// Warps 8-15 take the registers that the others give up (setmaxnreg: 56 + 88 + 2 x 184 of
-// 4 x 128).  Every wait is bounded (GPTQ_ERR_TIMEOUT).  No TMA multicast.
+//                registers: y += s_g P_g, two at a time;
+//   warp 16      TMA: X8 tile (TT tokens x 128 bytes, 128-byte swizzle) and packed words
+//                (4 BITS words x 128 rows) into a ring of stages;
+//   warp 17      MMA issuer: per quantization group one accumulator segment, in a ring of
+//                accumulators of tensor memory;
+//   warp 18      the groups' fp16 scales and packed zero points by asynchronous copies into a
+//                ring of their own (they outlive the stage: the epilogue scales later).
+// The epilogue takes registers that the others give up (setmaxnreg).  Every wait is bounded
+// (GPTQ_ERR_TIMEOUT).  No TMA multicast.
 //
-// Codes to e4m3: the values q - z of one group and row are a table of 2^BITS bytes in registers
-// that byte permutes index with the codes themselves: two lookups by the low three bits and a
-// third permute that picks by bit 3 for 4 bits, one lookup for 2 and 3 bits.
+// Codes to e4m3: a byte b < 16 read as e4m3 is b 2^-9 (the subnormals and the first binade are one
+// arithmetic sequence), so spreading the codes to bytes already gives q 2^-9, and 0x80 | z is -z 2^-9.
+// P_g 2^-9 = sum q 2^-9 X8 + sum (-z 2^-9) X8: the second sum takes the same MMAs again with an
+// operand of 32 equal columns.  That doubles the tensor work, which had three quarters of the time to
+// spare, and more than halves the converters' integer work, which bound the kernel: looking q - z up
+// in registers by byte permutes took 11 instructions for 8 codes against 5 (4096 x 4096 x 2048
+// tokens: 83 us against 78 us).
 //
 // Few tiles: the K range is split over a cluster of S CTAs, whose partial sums are joined
 // through distributed shared memory in rank order.
@@ -33,13 +40,22 @@
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "common.cuh"
 #include "pack.cuh"
 
 namespace gq {
 
-constexpr int D8_THREADS = 512;
-constexpr int D8_AST = 4, D8_ND = 3;
+constexpr int D8_THREADS = 640;
+constexpr int D8_EPI_WARP0 = 8, D8_PROD_WARP = 16;   // converters 0-7, epilogue 8-15, TMA 16, MMA 17, scales 18
+constexpr int D8_AST = 3, D8_PST = 4, D8_LAG = 2;
+// Registers a thread after setmaxnreg, per warpgroup.  A split above what the launch gave would wait
+// forever, so the launch checks that the kernel was compiled to D8_REGS.
+constexpr int D8_REGS = 96, D8_REGS_CONV = 72, D8_REGS_EPI = 136, D8_REGS_MISC = 64;
+static_assert(2 * D8_REGS_CONV + 2 * D8_REGS_EPI + D8_REGS_MISC <= D8_THREADS / 128 * D8_REGS, "register split");
+constexpr int D8_PAR_S = 1024, D8_PAR_Z = 256;   // bytes of scales and zero points of four groups
 constexpr int D8_SEG_TILES = 4;   // K tiles per segment for one group per row: 16 MMAs in place
 
 template <int BITS, int TT>
@@ -48,16 +64,21 @@ struct D8Cfg {
     static constexpr int X_BYTES = TT * 128;
     static constexpr int P_BYTES = KW * 128 * 4;
     static constexpr int STAGE_BYTES = X_BYTES + P_BYTES;
-    static constexpr int FIT = (220 * 1024) / STAGE_BYTES;
+    static constexpr int FIT = (206 * 1024) / STAGE_BYTES;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-    static constexpr int H = TT == 256 ? 2 : 1;       // accumulators per segment
-    static constexpr int DW = TT / H;                 // tokens per accumulator
     static constexpr int C = TT / 2;                  // tokens per epilogue warp
-    static constexpr int A_COL = D8_ND * 128;         // A ring behind the accumulators
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256 + 4 * TT + 512;
+    static constexpr int ND = 384 / TT;               // accumulators, at most (see acc_cols)
+    static constexpr int SMEM =
+        1024 + STAGES * STAGE_BYTES + D8_PST * (D8_PAR_S + D8_PAR_Z) + 4 * TT + 512;
     static_assert(STAGE_BYTES % 1024 == 0, "the swizzled tiles stay 1024-byte aligned");
     static_assert(TT * 128 * 4 <= STAGES * STAGE_BYTES, "partial sums fit the ring");
 };
+
+// Tensor memory: accumulators in front, then a ring of D8_AST operands: 32 columns of codes and 8 for
+// each group's zero point.
+__host__ __device__ constexpr int d8_acc_cols(int spt) { return spt <= 1 ? 384 : 256; }
+__host__ __device__ constexpr int d8_a_cols(int spt) { return 32 + 8 * (spt > 1 ? spt : 1); }
+static_assert(d8_acc_cols(1) + D8_AST * d8_a_cols(1) <= 512 && d8_acc_cols(4) + D8_AST * d8_a_cols(4) <= 512, "TMEM");
 
 struct D8Args {
     const __half* scales;    // [n_groups, N]
@@ -79,6 +100,27 @@ __device__ __forceinline__ void umma_e4m3_ta(uint32_t d, uint32_t a, uint64_t bd
         "r"(a), "l"(bdesc), "r"(idesc), "r"(acc));
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// 32 lanes x 16 consecutive columns, one column per register.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// 32 lanes x 8 consecutive columns, one column per register.
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(s));
@@ -98,40 +140,45 @@ __device__ __forceinline__ uint32_t codes_to_nibbles(uint32_t v) {
     }
     return v;
 }
-// Table bytes of eight nibble codes, in order.
+// The 32 codes of BITS words as 8 words of one code per byte.
 template <int BITS>
-__device__ __forceinline__ void table_bytes(uint32_t nib, const uint4& t, uint32_t& b0, uint32_t& b1) {
-    if constexpr (BITS == 4) {
-        const uint32_t m = nib & 0x77777777u, k = ((nib >> 1) & 0x44444444u) | 0x32103210u;
-        b0 = byte_perm(byte_perm(t.x, t.y, m), byte_perm(t.z, t.w, m), k);
-        b1 = byte_perm(byte_perm(t.x, t.y, m >> 16), byte_perm(t.z, t.w, m >> 16), k >> 16);
-    } else {
-        b0 = byte_perm(t.x, t.y, nib);
-        b1 = byte_perm(t.x, t.y, nib >> 16);
-    }
-}
-// The 32 codes of BITS words as 8 words of table bytes.
-template <int BITS>
-__device__ __forceinline__ void table_bytes_32(const uint32_t (&w)[BITS], const uint4& t, uint32_t* out) {
+__device__ __forceinline__ void codes_to_bytes(const uint32_t (&w)[BITS], uint32_t* out) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        uint32_t v;
+        uint32_t v;   // eight codes, one per nibble
         if constexpr (BITS == 4)
             v = w[c];
         else if constexpr (BITS == 2)
-            v = (w[c >> 1] >> (16 * (c & 1))) & 0xFFFFu;
+            v = codes_to_nibbles<2>((w[c >> 1] >> (16 * (c & 1))) & 0xFFFFu);
         else
-            v = (c == 0 ? w[0] : c == 3 ? w[2] >> 8 : __funnelshift_r(w[c - 1], w[c], c == 1 ? 24 : 16)) & 0xFFFFFFu;
-        table_bytes<BITS>(codes_to_nibbles<BITS>(v), t, out[2 * c], out[2 * c + 1]);
+            v = codes_to_nibbles<3>(
+                (c == 0 ? w[0] : c == 3 ? w[2] >> 8 : __funnelshift_r(w[c - 1], w[c], c == 1 ? 24 : 16)) & 0xFFFFFFu);
+        const uint32_t even = v & 0x0F0F0F0Fu, odd = (v >> 4) & 0x0F0F0F0Fu;
+        out[2 * c] = byte_perm(even, odd, 0x5140u);
+        out[2 * c + 1] = byte_perm(even, odd, 0x7362u);
     }
 }
 
-__device__ __forceinline__ void fma2(float2& acc, float s, uint32_t a, uint32_t b) {
-    asm("{\n\t.reg .b64 s, v, c;\n\t"
-        "mov.b64 s, {%2, %2};\n\tmov.b64 v, {%3, %4};\n\tmov.b64 c, {%0, %1};\n\t"
-        "fma.rn.f32x2 c, s, v, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
-        : "+f"(acc.x), "+f"(acc.y)
-        : "f"(s), "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+// Pairs of fp32 in one 64-bit register: acc += s * v for both halves.
+using pair_t = unsigned long long;
+__device__ __forceinline__ pair_t pair(uint32_t lo, uint32_t hi) {
+    pair_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    return v;
+}
+__device__ __forceinline__ void fma2(pair_t& acc, pair_t s, pair_t v) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(s), "l"(v));
+}
+__device__ __forceinline__ float pair_get(pair_t v, int hi) {
+    return __uint_as_float((uint32_t)(hi ? v >> 32 : v));
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, uint32_t src_bytes) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -159,23 +206,50 @@ __device__ __forceinline__ void store_y(void* Y, int bf16, long long at, float y
         reinterpret_cast<float*>(Y)[at] = y;
 }
 
+// One lane's column of C rows of Y, scaled; rows past the end are left alone.
+__device__ __forceinline__ void put(float* y, float v) { *y = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
+template <int C, typename YT>
+__device__ __forceinline__ void store_rows(YT* y, int ld, int rows, const pair_t (&acc)[C / 2], const float* xs) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        if (j < rows) put(y, pair_get(acc[j / 2], j & 1) * xs[j]);
+        y += ld;
+    }
+}
+
+// A warp waits for up to three barriers (those with a true, warp-uniform flag).  They are tried
+// together, so that their latencies overlap.  Every lane waits: lanes must not part ways in front of
+// the tcgen05 loads and stores, which need the warp converged.  Warp-uniform.
+__device__ __forceinline__ bool warp_wait(int where, uint64_t* b0, uint32_t p0, bool w0, uint64_t* b1, uint32_t p1,
+                                          bool w1, uint64_t* b2, uint32_t p2, bool w2) {
+    const bool r0 = !w0 || mbar_try_wait(b0, p0), r1 = !w1 || mbar_try_wait(b1, p1), r2 = !w2 || mbar_try_wait(b2, p2);
+    return __all_sync(~0u, (r0 || mbar_wait(b0, p0, where)) && (r1 || mbar_wait(b1, p1, where)) &&
+                               (r2 || mbar_wait(b2, p2, where)));
+}
+__device__ __forceinline__ bool warp_wait(int where, uint64_t* b, uint32_t p) {
+    return __all_sync(~0u, mbar_wait(b, p, where));
+}
+
 template <int BITS, int TT>
 __global__ void __launch_bounds__(D8_THREADS, 1)
     dq_gemm_e4m3_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mP, const D8Args p) {
     using Cfg = D8Cfg<BITS, TT>;
-    constexpr int STAGES = Cfg::STAGES, H = Cfg::H, DW = Cfg::DW, C = Cfg::C;
+    constexpr int STAGES = Cfg::STAGES, C = Cfg::C, ND = Cfg::ND;
 
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint4* lut = reinterpret_cast<uint4*>(smem + STAGES * Cfg::STAGE_BYTES);   // [16] table of each zero point
-    float* xs = reinterpret_cast<float*>(lut + 16);                            // [TT] scales of the tile's tokens
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset, so that accesses stay shared-memory ones
+    uint8_t* par = smem + STAGES * Cfg::STAGE_BYTES;   // [PST] scales [4][128] fp16, zero points [4][16] words
+    float* xs = reinterpret_cast<float*>(par + D8_PST * (D8_PAR_S + D8_PAR_Z));   // [TT] scales of the tile's tokens
     uint64_t* full = reinterpret_cast<uint64_t*>(xs + TT);   // [STAGES] TMA landed
     uint64_t* empty = full + STAGES;                         // [STAGES] MMAs of the stage done
     uint64_t* conv = empty + STAGES;                         // [AST] A operand written
     uint64_t* aempty = conv + D8_AST;                        // [AST] A operand read
     uint64_t* dfull = aempty + D8_AST;                       // [ND] segment complete
-    uint64_t* dempty = dfull + D8_ND;                        // [ND] segment drained
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + D8_ND);
+    uint64_t* dempty = dfull + ND;                        // [ND] segment drained
+    uint64_t* pfull = dempty + ND;                        // [PST] scales and zero points landed
+    uint64_t* pempty = pfull + D8_PST;                       // [PST] read by converters and epilogue
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pempty + D8_PST);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -187,16 +261,15 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
             mbar_init(&conv[s], 4);
             mbar_init(&aempty[s], 1);
         }
-        for (int s = 0; s < D8_ND; ++s) {
+        for (int s = 0; s < ND; ++s) {
             mbar_init(&dfull[s], 1);
-            mbar_init(&dempty[s], 8 / H);
+            mbar_init(&dempty[s], 8);
+        }
+        for (int s = 0; s < D8_PST; ++s) {
+            mbar_init(&pfull[s], 1);
+            mbar_init(&pempty[s], 16);
         }
         fence_mbar_init();
-    }
-    if (threadIdx.x < 256) {   // byte c of table z: e4m3(c - z)
-        const int z = threadIdx.x >> 4, c = threadIdx.x & 15;
-        reinterpret_cast<uint8_t*>(lut)[threadIdx.x] =
-            (uint8_t)__nv_cvt_float_to_fp8((float)(c - z), __NV_SATFINITE, __NV_E4M3);
     }
     if (warp == 0) {
         __syncwarp();
@@ -209,200 +282,155 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
 
+    const uint32_t a_ring = tmem + d8_acc_cols(p.spt), a_cols = d8_a_cols(p.spt);
+    const uint32_t nd = d8_acc_cols(p.spt) / TT;   // accumulators in use
+
     // K tiles of this CTA, and the segments in them
     const int rank = p.split > 1 ? (int)cluster_rank() : 0;
     const int nkt_all = (p.K + 127) / 128;
     const int kt0 = (int)((long long)nkt_all * rank / p.split);
-    const int kt1 = (int)((long long)nkt_all * (rank + 1) / p.split);
-    const int nkt = kt1 - kt0;
+    const int nkt = (int)((long long)nkt_all * (rank + 1) / p.split) - kt0;
     const int step = (int)gridDim.x / p.split, first = (int)blockIdx.x / p.split;
     // the last K tile may hold fewer groups than spt
-    const int nseg = p.spt ? min(kt1 * p.spt, p.K / (128 / p.spt)) - kt0 * p.spt
+    const int nseg = p.spt ? min((kt0 + nkt) * p.spt, p.K / (128 / p.spt)) - kt0 * p.spt
                            : (nkt + D8_SEG_TILES - 1) / D8_SEG_TILES;
 
-    if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 0 && lane == 0) {
-            // ---------------- TMA producer
-            prefetch_tmap(&mX);
-            prefetch_tmap(&mP);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int w = first; w < p.tiles && ok; w += step) {
-                const int n0 = (w % p.tiles_n) * 128, m0 = (w / p.tiles_n) * TT;
-                for (int kt = kt0; kt < kt1; ++kt, ++it) {
-                    const uint32_t s = it % STAGES;
-                    if (!mbar_wait(&empty[s], ((it / STAGES) & 1) ^ 1, w)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = smem + s * Cfg::STAGE_BYTES;
-                    mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
-                    tma_load_2d(st + Cfg::X_BYTES, &mP, &full[s], n0, kt * Cfg::KW);
-                    tma_load_2d(st, &mX, &full[s], kt * 128, m0);
-                }
-            }
-            // after a wait that ran out, the copies still in flight land before the CTA leaves
-            for (uint32_t b = it > STAGES ? it - STAGES : 0; !ok && b < it; ++b)
-                (void)mbar_wait(&full[b % STAGES], (b / STAGES) & 1, -1);
-        } else if (warp == 1 && lane == 0) {
-            // ---------------- MMA issuer
-            constexpr uint32_t idesc = make_idesc(0u, 128, DW);   // e4m3 x e4m3 -> fp32
-            uint32_t it = 0, seg = 0;
-            bool ok = true;
-            for (int w = first; w < p.tiles && ok; w += step) {
-                for (int kt = 0; kt < nkt && ok; ++kt, ++it) {
-                    const uint32_t s = it % STAGES, a = it % D8_AST;
-                    if (!mbar_wait(&full[s], (it / STAGES) & 1, w) || !mbar_wait(&conv[a], (it / D8_AST) & 1, w)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t xb = smem_u32(smem + s * Cfg::STAGE_BYTES);
-                    const uint32_t at = tmem + Cfg::A_COL + 32 * a;
-                    const int segs = p.spt ? min(p.spt, nseg - kt * p.spt) : 1;
-                    const int mmas = p.spt ? 4 / p.spt : 4;
-                    const bool open = p.spt || kt % D8_SEG_TILES == 0;
-                    const bool close = p.spt || kt % D8_SEG_TILES == D8_SEG_TILES - 1 || kt == nkt - 1;
-                    for (int sg = 0; sg < segs && ok; ++sg) {
-#pragma unroll
-                        for (int h = 0; h < H; ++h) {
-                            const uint32_t dc = seg * H + h, buf = dc % D8_ND;
-                            if (open) {
-                                if (!mbar_wait(&dempty[buf], ((dc / D8_ND) & 1) ^ 1, w)) {
-                                    ok = false;
-                                    break;
-                                }
-                                tc_fence_after();
-                            }
-                            for (int j = 0; j < mmas; ++j) {
-                                const int kk = sg * mmas + j;   // which 32 columns of the K tile
-                                umma_e4m3_ta(tmem + buf * 128, at + 8 * kk,
-                                             desc_sw128_kmajor(xb + h * (DW * 128) + 32 * kk), idesc,
-                                             (open && j == 0) ? 0u : 1u);
-                            }
-                            if (close) umma_commit(&dfull[buf]);
-                        }
-                        if (close) ++seg;
-                    }
-                    umma_commit(&empty[s]);
-                    umma_commit(&aempty[a]);
-                }
-            }
-        }
-    } else if (warp < 8) {
-        // ---------------- converters: thread t owns row n0 + t
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        const int t = threadIdx.x - 128, qd = warp & 3;
-        const long long zwords = ((long long)p.N * BITS + 31) / 32;
-        const int qps = p.spt ? 4 / p.spt : 4;    // 32-column quarters per table
-        uint32_t it = 0;
+    if (warp < D8_EPI_WARP0) {
+        // ---------------- converters: thread t of a set owns row n0 + t; the two sets take turns
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(D8_REGS_CONV));
+        const int qd = warp & 3, t = 32 * qd + lane;
+        const uint32_t set = warp >> 2;
+        const uint32_t a_row = a_ring + ((uint32_t)(32 * qd) << 16);
+        uint32_t it = 0, unit = 0;
         bool ok = true;
         for (int w = first; w < p.tiles && ok; w += step) {
-            const int n = (w % p.tiles_n) * 128 + t;
-            const bool live = p.qzeros != nullptr && n < p.N;
-            int z[4], zn[4];
-            // zero points of a K tile, fetched one tile ahead
-            auto fetch = [&](int kt, int (&zz)[4]) {
+            for (int kt = 0; kt < nkt; ++kt, ++it) {
+                // groups of this K tile, counted from the CTA's first: four to a unit
+                const int grp = kt * p.spt;
+                const uint8_t* zq = par + (unit % D8_PST) * (D8_PAR_S + D8_PAR_Z) + D8_PAR_S;
+                if ((it & 1) == set) {
+                    const uint32_t s = it % STAGES, a = it % D8_AST;
+                    ok = warp_wait(w, &full[s], (it / STAGES) & 1, true, &aempty[a], ((it / D8_AST) & 1) ^ 1, true,
+                                   &pfull[unit % D8_PST], (unit / D8_PST) & 1, true);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t* col =
+                        reinterpret_cast<const uint32_t*>(smem + s * Cfg::STAGE_BYTES + Cfg::X_BYTES) + t;
+                    const uint32_t dst = a_row + a_cols * a;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    zz[q] = 1 << (BITS - 1);
-                    const int gi = p.spt ? kt * p.spt + q / qps : 0;
-                    if (live && q % qps == 0 && (p.spt == 0 || gi * (128 / p.spt) < p.K))
-                        zz[q] = (int)stream_code(p.qzeros + gi * zwords, 1, n, BITS);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t words[2][BITS], r[16];
+#pragma unroll
+                        for (int i = 0; i < 2 * BITS; ++i) words[i / BITS][i % BITS] = col[(2 * BITS * h + i) * 128];
+                        codes_to_bytes<BITS>(words[0], r);
+                        codes_to_bytes<BITS>(words[1], r + 8);
+                        tmem_st_32x32b_x16(dst + 16 * h, r);
+                    }
+                    for (int q = 0; q < (p.spt ? p.spt : 1); ++q) {   // each group's zero point, -z 2^-9
+                        uint32_t z = 1u << (BITS - 1);
+                        if (p.qzeros != nullptr) {
+                            const uint32_t* zw = reinterpret_cast<const uint32_t*>(zq + 64 * ((grp + q) & 3));
+                            const int b = t * BITS;
+                            z = zw[b >> 5] >> (b & 31);
+                            if (BITS == 3 && (b & 31) > 29) z |= zw[(b >> 5) + 1] << (32 - (b & 31));
+                            z &= (1u << BITS) - 1u;
+                        }
+                        z = (0x80u | z) * 0x01010101u;
+                        const uint32_t r[8] = {z, z, z, z, z, z, z, z};
+                        tmem_st_32x32b_x8(dst + 32 + 8 * q, r);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&conv[a]);
                 }
-            };
-            fetch(kt0, zn);
-            for (int kt = kt0; kt < kt1; ++kt, ++it) {
-                const uint32_t s = it % STAGES, a = it % D8_AST;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) z[q] = zn[q];
-                if (p.spt && kt + 1 < kt1) fetch(kt + 1, zn);
-                if (!mbar_wait(&full[s], (it / STAGES) & 1, w) ||
-                    !mbar_wait(&aempty[a], ((it / D8_AST) & 1) ^ 1, w)) {
-                    ok = false;
-                    break;
+                if (kt == nkt - 1 || ((grp + p.spt) & 3) == 0 && p.spt) {   // the unit is used up
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pempty[unit % D8_PST]);
+                    ++unit;
                 }
-                tc_fence_after();
-                const uint32_t* col = reinterpret_cast<const uint32_t*>(smem + s * Cfg::STAGE_BYTES + Cfg::X_BYTES) + t;
-                uint32_t r[32];
-                uint4 tab = lut[z[0]];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t words[BITS];
-#pragma unroll
-                    for (int i = 0; i < BITS; ++i) words[i] = col[(q * BITS + i) * 128];
-                    if (q > 0 && q % qps == 0) tab = lut[z[q]];
-                    table_bytes_32<BITS>(words, tab, r + 8 * q);
-                }
-                tmem_st_32x32b_x32(tmem + Cfg::A_COL + 32 * a + ((uint32_t)(32 * qd) << 16), r);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&conv[a]);
             }
         }
-    } else {
+    } else if (warp < D8_PROD_WARP) {
         // ---------------- epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        const int ew = warp - 8, qd = warp & 3, half = ew >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(D8_REGS_EPI));
+        const int ew = warp - D8_EPI_WARP0, qd = warp & 3, half = ew >> 2;
         const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
-        const uint32_t col0 = H == 2 ? 0 : (uint32_t)(half * C);   // columns of the accumulator
-        const int et = threadIdx.x - 256;
-        uint32_t seg = 0;
+        const uint32_t col0 = (uint32_t)(half * C);   // columns of the accumulator
+        const int et = threadIdx.x - 32 * D8_EPI_WARP0;
+        uint32_t buf = 0, dph = 0, unit = 0;   // accumulator and its phase
         bool ok = true;   // once false, the loop goes on without waiting: its barriers need every warp
         for (int w = first; w < p.tiles; w += step) {
             const int n = (w % p.tiles_n) * 128 + 32 * qd + lane, m0 = (w / p.tiles_n) * TT;
             asm volatile("bar.sync 1, 256;" ::: "memory");   // the previous tile's scales are read
             if (et < TT) xs[et] = m0 + et < p.M ? p.x_scale[m0 + et] : 0.f;
             asm volatile("bar.sync 1, 256;" ::: "memory");
-            float2 acc[C / 2];
+            pair_t acc[C / 2];
 #pragma unroll
-            for (int j = 0; j < C / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-            const long long g0 = p.spt ? (long long)kt0 * p.spt : 0;
-            const __half* sp = p.scales + g0 * p.N + n;
-            float s_next = n < p.N ? __half2float(sp[0]) : 0.f;
-            for (int sg = 0; sg < nseg && ok; ++sg, ++seg) {
-                const float s = s_next;
-                if (p.spt && sg + 1 < nseg && n < p.N) {
-                    sp += p.N;
-                    s_next = __half2float(*sp);
+            for (int j = 0; j < C / 2; ++j) acc[j] = 0;
+            // the scale of group g
+            const int groups = p.spt ? nseg : 1;
+            auto scale = [&](int g) {
+                if ((g & 3) == 0) ok = warp_wait(w, &pfull[unit % D8_PST], (unit / D8_PST) & 1);
+                const __half h = reinterpret_cast<const __half*>(
+                    par + (unit % D8_PST) * (D8_PAR_S + D8_PAR_Z))[128 * (g & 3) + 32 * qd + lane];
+                if ((g & 3) == 3 || g == groups - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pempty[unit % D8_PST]);
+                    __syncwarp();
+                    ++unit;
                 }
-                const uint32_t dc = H == 2 ? seg * 2 + half : seg, buf = dc % D8_ND;
-                ok = mbar_wait(&dfull[buf], (dc / D8_ND) & 1, w);
+                return h;
+            };
+            __half s_next = __float2half(0.f);
+            if (ok) s_next = scale(0);
+            for (int sg = 0; sg < nseg && ok; ++sg) {
+                const uint32_t sf = __float_as_uint(512.f * __half2float(s_next));   // P_g comes as 2^-9 P_g
+                const pair_t s = pair(sf, sf);
+                ok = warp_wait(w, &dfull[buf], dph);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < C / 32; ++c) {
                     uint32_t r[32];
-                    tmem_ld_32x32b_x32(tmem + buf * 128 + col0 + 32 * c + lane_off, r);
+                    tmem_ld_32x32b_x32(tmem + buf * TT + col0 + 32 * c + lane_off, r);
+                    if (c == 0 && sg + 1 < groups) s_next = scale(sg + 1);
                     tmem_ld_wait();
+                    if (c == C / 32 - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&dempty[buf]);
+                        __syncwarp();
+                    }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, r[2 * j], r[2 * j + 1]);
+                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, pair(r[2 * j], r[2 * j + 1]));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&dempty[buf]);
+                if (++buf == nd) {
+                    buf = 0;
+                    dph ^= 1;
+                }
             }
             const int j0 = half * C;   // this warp's first token of the tile
             if (p.split == 1) {
                 if (ok && n < p.N) {
-#pragma unroll
-                    for (int j = 0; j < C; ++j)
-                        if (m0 + j0 + j < p.M)
-                            store_y(p.Y, p.y_bf16, (long long)(m0 + j0 + j) * p.N + n,
-                                    ((j & 1) ? acc[j / 2].y : acc[j / 2].x) * xs[j0 + j]);
+                    const int rows = p.M - m0 - j0;
+                    const long long at = (long long)(m0 + j0) * p.N + n;
+                    if (p.y_bf16)
+                        store_rows<C>(reinterpret_cast<__nv_bfloat16*>(p.Y) + at, p.N, rows, acc, xs + j0);
+                    else
+                        store_rows<C>(reinterpret_cast<float*>(p.Y) + at, p.N, rows, acc, xs + j0);
                 }
             } else {
                 // One tile per cluster.  The partial sums take the ring's place once the last MMAs
-                // have read it (a segment of one half completes before those of the other).
+                // have read it.
                 float* red = reinterpret_cast<float*>(smem);   // [TT][128]
                 if (ok) ok = mbar_wait(&empty[(nkt - 1) % STAGES], ((nkt - 1) / STAGES) & 1, w);
                 if (ok) {
 #pragma unroll
                     for (int j = 0; j < C; ++j)
-                        red[(j0 + j) * 128 + 32 * qd + lane] = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
+                        red[(j0 + j) * 128 + 32 * qd + lane] = pair_get(acc[j / 2], j & 1);
                 }
+                __syncwarp();
                 cluster_sync_all();
                 // rank r finishes the tokens r, r + split, ...
                 const int c = et & 127, nn = (w % p.tiles_n) * 128 + c;
@@ -414,13 +442,140 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                         store_y(p.Y, p.y_bf16, (long long)(m0 + j) * p.N + nn, y * xs[j]);
                     }
                 }
+                __syncwarp();
                 cluster_sync_all();   // no CTA leaves while its partial sums are being read
             }
         }
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(D8_REGS_MISC));
+      if (warp == D8_PROD_WARP && lane == 0) {
+        // ---------------- producer: X8 and packed words by TMA
+        prefetch_tmap(&mX);
+        prefetch_tmap(&mP);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int w = first; w < p.tiles && ok; w += step) {
+            const int n0 = (w % p.tiles_n) * 128, m0 = (w / p.tiles_n) * TT;
+            for (int kt = 0; kt < nkt; ++kt, ++it) {
+                const uint32_t s = it % STAGES;
+                ok = mbar_wait(&empty[s], ((it / STAGES) & 1) ^ 1, w);
+                if (!ok) break;
+                uint8_t* st = smem + s * Cfg::STAGE_BYTES;
+                mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
+                tma_load_2d(st + Cfg::X_BYTES, &mP, &full[s], n0, (kt0 + kt) * Cfg::KW);
+                tma_load_2d(st, &mX, &full[s], (kt0 + kt) * 128, m0);
+            }
+        }
+        // after a wait that ran out, the copies still in flight land before the CTA leaves
+        for (uint32_t b = it > STAGES ? it - STAGES : 0; !ok && b < it; ++b)
+            (void)mbar_wait(&full[b % STAGES], (b / STAGES) & 1, -1);
+      } else if (warp == D8_PROD_WARP + 2) {
+        // ---------------- scales and zero points, four groups to a unit, by asynchronous copies of
+        // 16 and 4 bytes a lane; a unit is handed over when it has landed, D8_LAG units later, so
+        // that the copies overlap
+        const long long zwords = ((long long)p.N * BITS + 31) / 32;
+        const int groups = p.spt ? nseg : 1;
+        uint32_t it = 0, done = 0;
+        bool ok = true;
+        auto hand_over = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[done % D8_PST]);
+            ++done;
+        };
+        for (int w = first; w < p.tiles && ok; w += step) {
+            const int n = (w % p.tiles_n) * 128 + 8 * lane;
+            const long long zk = (long long)(w % p.tiles_n) * (4 * BITS) + lane;
+            const uint32_t s_bytes = lane < 16 && n < p.N ? 16 : 0, z_bytes = zk < zwords ? 4 : 0;
+            const long long g0 = p.spt ? (long long)kt0 * p.spt : 0;
+            const __half* sp = p.scales + g0 * p.N + (s_bytes ? n : 0);
+            const int32_t* zp = p.qzeros + g0 * zwords + (z_bytes ? zk : 0);
+            const bool zlane = p.qzeros != nullptr && lane < 4 * BITS;
+            for (int g = 0; g < groups; g += 4, ++it) {
+                ok = warp_wait(w, &pempty[it % D8_PST], ((it / D8_PST) & 1) ^ 1);
+                if (!ok) break;
+                const uint32_t dst = smem_u32(par + (it % D8_PST) * (D8_PAR_S + D8_PAR_Z));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (g + q < groups) {
+                        if (lane < 16) cp_async_zfill<16>(dst + 256 * q + 16 * lane, sp, s_bytes);
+                        if (zlane) cp_async_zfill<4>(dst + D8_PAR_S + 64 * q + 4 * lane, zp, z_bytes);
+                        sp += p.N;
+                        zp += zwords;
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (it >= D8_LAG) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(D8_LAG) : "memory");
+                    hand_over();
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        while (done < it) hand_over();
+      } else if (warp == D8_PROD_WARP + 1) {
+        // ---------------- MMA issuer: the whole warp waits, one elected lane issues
+        constexpr uint32_t idesc = make_idesc(0u, 128, TT);   // e4m3 x e4m3 -> fp32
+        const bool lead = elect_one();
+        uint32_t it = 0, buf = 0, dph = 1;
+        bool ok = true;
+        // One K tile: MM = MMAs (32 columns each) per segment.  A segment of every group opens
+        // and closes within the tile; with one group per row it spans D8_SEG_TILES tiles.
+        // The barriers are tried together and every descriptor is a constant away from the
+        // stage's, as each wait or chain of address arithmetic costs the issuer about 100 clocks.
+        auto issue = [&](auto mm, uint32_t s, uint32_t a, int segs, bool open, bool close, int w) {
+            constexpr int MM = decltype(mm)::value;
+            const uint64_t xdesc = desc_sw128_kmajor(smem_u32(smem + s * Cfg::STAGE_BYTES));
+            const uint32_t at = a_ring + a_cols * a;
+#pragma unroll
+            for (int sg = 0; sg < 4 / MM; ++sg) {
+                if (sg >= segs) break;
+                // the converters' arrival on conv follows their own wait for the stage's TMA
+                // copies, X8 included
+                if (!warp_wait(w, &conv[a], (it / D8_AST) & 1, sg == 0, &dempty[buf], dph, open, &dempty[buf], dph,
+                               false))
+                    return false;
+                tc_fence_after();
+                if (lead) {
+                    const uint32_t d = tmem + buf * TT;
+#pragma unroll
+                    for (int j = 0; j < MM; ++j)
+                        umma_e4m3_ta(d, at + 8 * (sg * MM + j), xdesc + (uint64_t)(2 * (sg * MM + j)), idesc,
+                                     j > 0 ? 1u : open ? 0u : 1u);
+#pragma unroll
+                    for (int j = 0; j < MM; ++j)
+                        umma_e4m3_ta(d, at + 32 + 8 * sg, xdesc + (uint64_t)(2 * (sg * MM + j)), idesc, 1u);
+                    if (close) umma_commit(&dfull[buf]);
+                }
+                if (lead && sg == segs - 1) {
+                    umma_commit(&empty[s]);
+                    umma_commit(&aempty[a]);
+                }
+                if (close && ++buf == nd) {
+                    buf = 0;
+                    dph ^= 1;
+                }
+            }
+            return true;
+        };
+        for (int w = first; w < p.tiles && ok; w += step) {
+            for (int kt = 0; kt < nkt && ok; ++kt, ++it) {
+                const uint32_t s = it % STAGES, a = it % D8_AST;
+                if (p.spt <= 1) {
+                    const bool open = p.spt || kt % D8_SEG_TILES == 0;
+                    const bool close = p.spt || kt % D8_SEG_TILES == D8_SEG_TILES - 1 || kt == nkt - 1;
+                    ok = issue(std::integral_constant<int, 4>{}, s, a, 1, open, close, w);
+                } else {
+                    const int segs = min(p.spt, nseg - kt * p.spt);
+                    ok = p.spt == 2 ? issue(std::integral_constant<int, 2>{}, s, a, segs, true, true, w)
+                                    : issue(std::integral_constant<int, 1>{}, s, a, segs, true, true, w);
+                }
+            }
+        }
+    }
     }
     __syncwarp();
-    if (warp < 8 && p.split > 1) {   // the other warps' part in the epilogue's cluster barriers
-        cluster_sync_all();
+    if (p.split > 1 && (warp < D8_EPI_WARP0 || warp >= D8_PROD_WARP)) {
+        cluster_sync_all();   // these warps' part in the epilogue's cluster barriers
         cluster_sync_all();
     }
     tc_fence_before();
@@ -454,14 +609,17 @@ inline bool tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// MaxDynamicSharedMemorySize of one kernel, set once per device; safe from several threads (the
-// attribute is set again if two race, which changes nothing).
+// MaxDynamicSharedMemorySize of one kernel, set once per device, after a look at the registers that
+// its setmaxnreg split relies on; safe from several threads (setting it twice changes nothing).
 template <auto Kernel, int BYTES>
-cudaError_t smem_attr_once() {
+cudaError_t d8_prepare() {
     static std::atomic<bool> done[128];
     int dev = 0;
     GQ_TRY(cudaGetDevice(&dev));
     if (dev < 128 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaFuncAttributes at;
+    GQ_TRY(cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(Kernel)));
+    if (at.numRegs != gq::D8_REGS) return cudaErrorInvalidKernelImage;
     GQ_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 BYTES));
     if (dev < 128) done[dev].store(true, std::memory_order_release);
@@ -479,7 +637,7 @@ cudaError_t dq_gemm_e4m3_launch(const uint8_t* X8, const int32_t* qweight, gq::D
                  (uint64_t)p.N, Cfg::KW, 128, false))
         return cudaErrorInvalidValue;
     constexpr auto kern = gq::dq_gemm_e4m3_kernel<BITS, TT>;
-    GQ_TRY((smem_attr_once<kern, Cfg::SMEM>()));
+    GQ_TRY((d8_prepare<kern, Cfg::SMEM>()));
     p.tiles_n = (p.N + 127) / 128;
     const long long tiles = (long long)p.tiles_n * ((p.M + TT - 1) / TT);
     if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
@@ -507,8 +665,7 @@ cudaError_t dq_gemm_e4m3_launch(const uint8_t* X8, const int32_t* qweight, gq::D
 template <int BITS>
 cudaError_t dq_gemm_e4m3_run(const uint8_t* X8, const int32_t* qweight, const gq::D8Args& p, cudaStream_t st) {
     if (p.M <= 64) return dq_gemm_e4m3_launch<BITS, 64>(X8, qweight, p, st);
-    if (p.M <= 128) return dq_gemm_e4m3_launch<BITS, 128>(X8, qweight, p, st);
-    return dq_gemm_e4m3_launch<BITS, 256>(X8, qweight, p, st);
+    return dq_gemm_e4m3_launch<BITS, 128>(X8, qweight, p, st);
 }
 
 }  // namespace gqh
