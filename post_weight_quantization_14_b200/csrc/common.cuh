@@ -252,6 +252,27 @@ __host__ __device__ constexpr uint32_t make_idesc(uint32_t ab_format, int M, int
            ((uint32_t)(M >> 4) << 24);
 }
 
+// ----------------------------------------------------------------------------
+// Thread-block clusters
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+        : "=f"(v)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // tf32 split: x = hi + lo with hi = tf32(x) (round to nearest, ties away from zero) and
 // lo = tf32(x - hi).  The rounding works on the bit pattern: adding half a unit of the 13
 // dropped mantissa bits to the sign-magnitude encoding and clearing them rounds the

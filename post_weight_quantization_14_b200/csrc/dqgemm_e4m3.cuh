@@ -126,20 +126,6 @@ __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(s));
     return r;
 }
-// Eight BITS-wide codes in the low 8 BITS bits of v, one per nibble.
-template <int BITS>
-__device__ __forceinline__ uint32_t codes_to_nibbles(uint32_t v) {
-    if constexpr (BITS == 2) {
-        v = (v | (v << 8)) & 0x00FF00FFu;
-        v = (v | (v << 4)) & 0x0F0F0F0Fu;
-        v = (v | (v << 2)) & 0x33333333u;
-    } else if constexpr (BITS == 3) {
-        v = (v & 0x00000FFFu) | ((v & 0x00FFF000u) << 4);
-        v = (v & 0x003F003Fu) | ((v & 0x0FC00FC0u) << 2);
-        v = (v & 0x07070707u) | ((v & 0x38383838u) << 1);
-    }
-    return v;
-}
 // The 32 codes of BITS words as 8 words of one code per byte.
 template <int BITS>
 __device__ __forceinline__ void codes_to_bytes(const uint32_t (&w)[BITS], uint32_t* out) {
@@ -179,31 +165,6 @@ __device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, ui
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-        : "=f"(v)
-        : "r"(addr), "r"(rank)
-        : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void store_y(void* Y, int bf16, long long at, float y) {
-    if (bf16)
-        reinterpret_cast<__nv_bfloat16*>(Y)[at] = __float2bfloat16_rn(y);
-    else
-        reinterpret_cast<float*>(Y)[at] = y;
 }
 
 // One lane's column of C rows of Y, scaled; rows past the end are left alone.

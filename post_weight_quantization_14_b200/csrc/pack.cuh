@@ -3,6 +3,8 @@
 // each row's codes form a little-endian stream, code j at bits j*b .. j*b+b-1,
 // cut into 32-bit words; a 3-bit code may straddle two words.
 #pragma once
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 
 namespace gq {
@@ -48,6 +50,27 @@ __device__ __forceinline__ uint32_t stream_code(const int32_t* words, long long 
     uint64_t v = (uint32_t)words[k * word_stride];
     if (sh + bits > 32) v |= (uint64_t)(uint32_t)words[(k + 1) * word_stride] << 32;
     return (uint32_t)(v >> sh) & ((1u << bits) - 1u);
+}
+
+// Eight BITS-wide codes in the low 8 BITS bits of v, one per nibble.
+template <int BITS>
+__device__ __forceinline__ uint32_t codes_to_nibbles(uint32_t v) {
+    if constexpr (BITS == 2) {
+        v = (v | (v << 8)) & 0x00FF00FFu;
+        v = (v | (v << 4)) & 0x0F0F0F0Fu;
+        v = (v | (v << 2)) & 0x33333333u;
+    } else if constexpr (BITS == 3) {
+        v = (v & 0x00000FFFu) | ((v & 0x00FFF000u) << 4);
+        v = (v & 0x003F003Fu) | ((v & 0x0FC00FC0u) << 2);
+        v = (v & 0x07070707u) | ((v & 0x38383838u) << 1);
+    }
+    return v;
+}
+__device__ __forceinline__ void store_y(void* Y, int bf16, long long at, float y) {
+    if (bf16)
+        reinterpret_cast<__nv_bfloat16*>(Y)[at] = __float2bfloat16_rn(y);
+    else
+        reinterpret_cast<float*>(Y)[at] = y;
 }
 
 // W_hat[o, c] = scale[g(c), o] * (q[o, c] - zero[g(c), o]); one thread per weight, row-major.
