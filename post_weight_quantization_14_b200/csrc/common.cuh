@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <utility>
 
 #include "../../include/gptq_b200.h"
@@ -132,6 +133,15 @@ __device__ __forceinline__ void bulk_wait() {
 // Generic-proxy shared-memory writes become visible to the async (TMA) proxy.
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// Asynchronous copy of BYTES (4, 8 or 16) bytes, the part past src_bytes filled with zeros.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, uint32_t src_bytes) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(src_bytes), "n"(BYTES)
+                     : "memory");
 }
 // Programmatic dependent launch.  pdl_wait() blocks until the grid this one depends on
 // has completed and its writes are visible (a no-op for an ordinary launch); every kernel
@@ -374,6 +384,20 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t r
 // operands that threads read element by element rather than the tensor cores.
 bool make_tmap_2d_plain(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
                         uint32_t box_rows, uint32_t box_cols);
+
+// MaxDynamicSharedMemorySize of one kernel, set once per device; safe from several threads (setting
+// it twice changes nothing).
+template <auto Kernel, int BYTES>
+cudaError_t smem_attr_once() {
+    static std::atomic<bool> done[128];
+    int dev = 0;
+    GQ_TRY(cudaGetDevice(&dev));
+    if (dev < 128 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    GQ_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                BYTES));
+    if (dev < 128) done[dev].store(true, std::memory_order_release);
+    return cudaSuccess;
+}
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (kernel, device, size).
 cudaError_t ensure_smem_attr(const void* func, int bytes);

@@ -40,7 +40,6 @@
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -157,14 +156,6 @@ __device__ __forceinline__ void fma2(pair_t& acc, pair_t s, pair_t v) {
 }
 __device__ __forceinline__ float pair_get(pair_t v, int hi) {
     return __uint_as_float((uint32_t)(hi ? v >> 32 : v));
-}
-
-template <int BYTES>
-__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, uint32_t src_bytes) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
 // One lane's column of C rows of Y, scaled; rows past the end are left alone.
@@ -570,21 +561,15 @@ inline bool tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// MaxDynamicSharedMemorySize of one kernel, set once per device, after a look at the registers that
-// its setmaxnreg split relies on; safe from several threads (setting it twice changes nothing).
-template <auto Kernel, int BYTES>
-cudaError_t d8_prepare() {
-    static std::atomic<bool> done[128];
-    int dev = 0;
-    GQ_TRY(cudaGetDevice(&dev));
-    if (dev < 128 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    cudaFuncAttributes at;
-    GQ_TRY(cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(Kernel)));
-    if (at.numRegs != gq::D8_REGS) return cudaErrorInvalidKernelImage;
-    GQ_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                BYTES));
-    if (dev < 128) done[dev].store(true, std::memory_order_release);
-    return cudaSuccess;
+// The setmaxnreg split relies on the registers that the kernel was launched with.
+template <auto Kernel>
+bool d8_registers_fit() {
+    static const bool fit = [] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(Kernel)) == cudaSuccess &&
+               at.numRegs == gq::D8_REGS;
+    }();
+    return fit;
 }
 
 int num_sms();
@@ -598,7 +583,8 @@ cudaError_t dq_gemm_e4m3_launch(const uint8_t* X8, const int32_t* qweight, gq::D
                  (uint64_t)p.N, Cfg::KW, 128, false))
         return cudaErrorInvalidValue;
     constexpr auto kern = gq::dq_gemm_e4m3_kernel<BITS, TT>;
-    GQ_TRY((d8_prepare<kern, Cfg::SMEM>()));
+    if (!d8_registers_fit<kern>()) return cudaErrorInvalidKernelImage;
+    GQ_TRY((smem_attr_once<kern, Cfg::SMEM>()));
     p.tiles_n = (p.N + 127) / 128;
     const long long tiles = (long long)p.tiles_n * ((p.M + TT - 1) / TT);
     if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;

@@ -5,9 +5,24 @@
 // with g(k) = k / g, or g_idx[k] for layers quantized in activation order.  X is bf16 (xs = 1)
 // or e4m3 with one fp32 scale per row.
 //
-// One lane per output row n; eight warps share the rows of a CTA and split the columns k in
-// equal runs, whose sums are joined through shared memory in a fixed order.  q - z and
-// s (q - z) (at most 11 + 8 significant bits) are exact in fp32; sums are fp32.
+// Two kernels:
+//
+// gemv_mma_kernel (groups of consecutive columns).  The work is one pass over the packed words, so
+// the design is about issue slots next to the loads: with fp32 FMAs every weight costs an unpack, a
+// subtraction and M multiplies, with the warp-level tensor instruction (16 x 8 x 16, fp32 sums) about
+// 1.4 instructions for any M up to 8.  (tcgen05 would need the unpacked weights in shared or tensor
+// memory first; here they stay in the registers that unpacked them.)  K order inside one instruction
+// is free as long as both operands agree, which makes the packed layout fit without any shuffle: a
+// thread's word of 8 codes (row n, columns k .. k + 7) is four pairs (i, i + 4) that mask out of the
+// word side by side, and its 16 bytes of X (token, k .. k + 7) are the matching pairs.  q - z is exact
+// in bf16 and fp16, P = X (q - z)^T is summed over a group and enters y as s P in fp32.
+// A CTA owns 128 rows n and a run of columns.  Words and X arrive in a ring of stages of 256 columns
+// by asynchronous copies, which keeps some 100 KB in flight on an SM without registers; four warps
+// take 32 rows each of a stage's first 128 columns, four of the others.  The halves' sums, and those of
+// the CTAs of a cluster that split K, are joined in a fixed order through shared memory.
+//
+// gemv_lane_kernel (g_idx, any column in any group).  One lane per row n; eight warps split the
+// columns.  s (q - z) (at most 11 + 8 significant bits) is exact in fp32.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -33,10 +48,12 @@ struct GemvArgs {
     int M;
     long long N, K;
     int g, ng;                // group length and count
+    int g_all;                // one group per row (g = K)
     int bits;
     unsigned nblocks;         // blocks of rows n
     unsigned split;           // CTAs of a cluster, which split K
     int vec;                  // N % 4 == 0: 16-byte loads of packed words
+    int gshift;               // log2 g, or 31 for one group per row
 };
 
 constexpr int GV_WARPS = 8, GV_TOK = 4;
@@ -113,34 +130,48 @@ __device__ __forceinline__ uint32_t bits_of(const T& v) {
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 
-// The eight columns k .. k + 7 of one token as the pairs (i, i + 4), i = 0 .. 3.
-__device__ __forceinline__ void x_pairs(const __nv_bfloat16* x, uint32_t (&b)[4]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(x);
-    b[0] = __byte_perm(u.x, u.z, 0x5410);
-    b[1] = __byte_perm(u.x, u.z, 0x7632);
-    b[2] = __byte_perm(u.y, u.w, 0x5410);
-    b[3] = __byte_perm(u.y, u.w, 0x7632);
+// A thread's eight columns of a step of one token, as loaded: k .. k + 7, or (two runs of four, groups
+// of 16) lo .. lo + 3 and hi .. hi + 3.
+template <typename XT>
+struct XRaw;
+template <>
+struct XRaw<__nv_bfloat16> {
+    uint4 u;
+};
+template <>
+struct XRaw<__nv_fp8_e4m3> {
+    uint2 u;
+};
+__device__ __forceinline__ XRaw<__nv_bfloat16> load_x8(const __nv_bfloat16* x) {
+    return {*reinterpret_cast<const uint4*>(x)};
 }
-__device__ __forceinline__ void x_pairs(const __nv_fp8_e4m3* x, uint32_t (&b)[4]) {   // e4m3 is exact in fp16
-    const uint2 u = *reinterpret_cast<const uint2*>(x);
+__device__ __forceinline__ XRaw<__nv_fp8_e4m3> load_x8(const __nv_fp8_e4m3* x) {
+    return {*reinterpret_cast<const uint2*>(x)};
+}
+__device__ __forceinline__ XRaw<__nv_bfloat16> load_x44(const __nv_bfloat16* lo, const __nv_bfloat16* hi) {
+    const uint2 a = *reinterpret_cast<const uint2*>(lo), b = *reinterpret_cast<const uint2*>(hi);
+    return {make_uint4(a.x, a.y, b.x, b.y)};
+}
+__device__ __forceinline__ XRaw<__nv_fp8_e4m3> load_x44(const __nv_fp8_e4m3* lo, const __nv_fp8_e4m3* hi) {
+    return {make_uint2(*reinterpret_cast<const uint32_t*>(lo), *reinterpret_cast<const uint32_t*>(hi))};
+}
+// The columns in pairs: (i, i + 4), i = 0 .. 3; or (0, 2), (1, 3) of the first four and of the second.
+template <bool G16>
+__device__ __forceinline__ void x_pairs(const XRaw<__nv_bfloat16>& r, uint32_t (&b)[4]) {
+    const uint32_t y = G16 ? r.u.y : r.u.z, z = G16 ? r.u.z : r.u.y;
+    b[0] = __byte_perm(r.u.x, y, 0x5410);
+    b[1] = __byte_perm(r.u.x, y, 0x7632);
+    b[2] = __byte_perm(z, r.u.w, 0x5410);
+    b[3] = __byte_perm(z, r.u.w, 0x7632);
+}
+template <bool G16>
+__device__ __forceinline__ void x_pairs(const XRaw<__nv_fp8_e4m3>& r, uint32_t (&b)[4]) {   // exact in fp16
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t two = __byte_perm(u.x, u.y, i | ((i + 4) << 4));   // bytes i and i + 4
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
-        b[i] = bits_of(h);
+        const uint32_t two = G16 ? __byte_perm(i < 2 ? r.u.x : r.u.y, 0, (i & 1) ? 0x4431 : 0x4420)
+                                 : __byte_perm(r.u.x, r.u.y, i | ((i + 4) << 4));
+        b[i] = bits_of(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3));
     }
-}
-
-// The four columns k .. k + 3 of one token as the pairs (0, 2) and (1, 3).
-__device__ __forceinline__ void x_quad(const __nv_bfloat16* x, uint32_t& b0, uint32_t& b1) {
-    const uint2 u = *reinterpret_cast<const uint2*>(x);
-    b0 = __byte_perm(u.x, u.y, 0x5410);
-    b1 = __byte_perm(u.x, u.y, 0x7632);
-}
-__device__ __forceinline__ void x_quad(const __nv_fp8_e4m3* x, uint32_t& b0, uint32_t& b1) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(x);
-    b0 = bits_of(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(__byte_perm(u, 0, 0x4420) & 0xFFFFu), __NV_E4M3));
-    b1 = bits_of(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(__byte_perm(u, 0, 0x4431) & 0xFFFFu), __NV_E4M3));
 }
 
 // q - z of one row's columns in pairs.  For up to 4 bits ``w`` holds the codes as nibbles and pair i is
@@ -206,213 +237,261 @@ __device__ __forceinline__ void quad_nibbles(uint32_t w, uint32_t w2, int sh, ui
 }
 template <int BITS>
 __device__ __forceinline__ uint32_t zero_pair(uint32_t z, __nv_bfloat16) {
-    const float f = (BITS <= 4 ? 128.f : 0.f) + (float)z;
-    return bits_of(__floats2bfloat162_rn(f, f));
+    if constexpr (BITS <= 4) return z * 0x00010001u | 0x43004300u;   // 128 + z, twice
+    return bits_of(__floats2bfloat162_rn((float)z, (float)z));
 }
 template <int BITS>
 __device__ __forceinline__ uint32_t zero_pair(uint32_t z, __nv_fp8_e4m3) {
-    return ((0x6400u | z) << 16) | 0x6400u | z;
+    return z * 0x00010001u | 0x64006400u;   // 1024 + z, twice
 }
 
-constexpr int GM_WARPS = 8;        // warps of a CTA, all on the same rows n
-constexpr int GM_UNIT = 128;       // columns of a unit: four steps of 32
+constexpr int GM_THREADS = 256;    // eight warps: four of 32 rows n each, times two runs of columns
+constexpr int GM_ROWS = 128;       // rows n of a CTA
+constexpr int GM_K = 256;          // columns of a stage, 128 for each half of the warps
+constexpr int GM_WSTRIDE = 4 * GM_ROWS + 32;   // bytes of a row of words: 16-byte reads without bank conflicts
 
-template <int BITS, typename XT, int MT, int NT, bool G16>
-__global__ void __launch_bounds__(32 * GM_WARPS, 2) gemv_mma_kernel(const GemvArgs p) {
-    constexpr int ROWS = 32 * NT, TOK = 8 * MT, TILES = 2 * NT;
-    constexpr int WPC = G16 ? (BITS == 3 ? 4 : 2) : BITS == 8 || BITS == 3 ? 2 : 1;   // words that hold a thread's eight codes
-    __shared__ float red[GM_WARPS][TOK][ROWS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+template <int BITS, typename XT, int MT>
+struct GmCfg {
+    static constexpr int TOK = 8 * MT;
+    static constexpr int WROWS = GM_K * BITS / 32;
+    static constexpr int W_BYTES = WROWS * GM_WSTRIDE;
+    // the reads of eight (16-byte) or sixteen (8-byte) lanes fall into different banks
+    static constexpr int XSTRIDE = GM_K * (int)sizeof(XT) + (sizeof(XT) == 2 ? 64 : 32);
+    static constexpr int STAGE = W_BYTES + TOK * XSTRIDE;
+    static constexpr int FIT = 110 * 1024 / STAGE;   // two CTAs to an SM
+    static constexpr int STAGES = FIT > 4 ? 4 : FIT < 2 ? 2 : FIT;
+    static constexpr int SUMS = 2 * TOK * GM_ROWS * 4;
+    static constexpr int SMEM = STAGES * STAGE > SUMS ? STAGES * STAGE : SUMS;
+};
+
+template <int BITS, typename XT, int MT, bool G16>
+__global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs p) {
+    using Cfg = GmCfg<BITS, XT, MT>;
+    constexpr int TOK = Cfg::TOK, STAGES = Cfg::STAGES;
+    constexpr int GROUPS = G16 ? 8 : 4;   // of 128 columns, at most
+    extern __shared__ __align__(128) uint8_t gm_smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
+    const int nw = warp & 3, kg = warp >> 2;
     const unsigned cta = blockIdx.x / p.split, rank = blockIdx.x % p.split;
-    const long long n0 = (long long)(cta % p.nblocks) * ROWS + 4 * gid;   // n0 + 32 i + 0 .. 3, i < NT
+    const long long nc = (long long)(cta % p.nblocks) * GM_ROWS;   // the CTA's first row
     const int m0 = (int)(cta / p.nblocks) * TOK;
     const int K = (int)p.K;
-    const long long zwords = (p.N * BITS + 31) / 32;
     const XT* X = reinterpret_cast<const XT*>(p.X);
+    const int nst = (K + GM_K - 1) / GM_K;
+    const int st0 = (int)((long long)nst * rank / p.split), st1 = (int)((long long)nst * (rank + 1) / p.split);
 
-    const int units = (K + GM_UNIT - 1) / GM_UNIT;
-    const int slot = (int)rank * GM_WARPS + warp, slots = (int)p.split * GM_WARPS;
-    const int u0 = (int)((long long)units * slot / slots), u1 = (int)((long long)units * (slot + 1) / slots);
-
-    float total[TILES][MT][4] = {}, part[TILES][MT][4] = {};
-    float sc[4 * NT];
-    uint32_t zz[4 * NT];
-    // Row ``r`` of the packed words, the thread's 4 NT rows n.
-    auto load_row = [&](long long r, bool valid, uint32_t (&w)[4 * NT]) {
-        const int32_t* src = p.qweight + r * p.N;
+    // ---- copies into the ring: BITS x 16 bytes of words and MT x 8 elements of X a thread and stage
+    const int wrows = (int)(((long long)K * BITS + 31) / 32);
+    const int lc = tid & 31, lr = tid >> 5;   // this thread's 16-byte column (8-element chunk of X) and first row
+    const int32_t* wsrc = p.qweight + ((long long)st0 * Cfg::WROWS + lr) * p.N + nc + 4 * lc;
+    const long long left = p.N - (nc + 4 * lc), step8 = 8 * p.N;   // rows n from this column on; words of 8 rows
+    const int wleft = left > 0 ? wrows - lr : 0;
+    auto issue = [&](int st) {
+        const uint32_t base = smem_u32(gm_smem) + (uint32_t)((st - st0) % STAGES) * Cfg::STAGE;
+        const uint32_t dst = base + (uint32_t)(lr * GM_WSTRIDE + 16 * lc);
+        const int rows = wleft - st * Cfg::WROWS;   // this thread's words in the stage: 8 i < rows
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const long long n = n0 + 32 * i;
+        for (int i = 0; i < BITS; ++i) {
             if (p.vec) {
-                const uint4 u = valid && n < p.N ? __ldg(reinterpret_cast<const uint4*>(src + n)) : make_uint4(0, 0, 0, 0);
-                w[4 * i] = u.x;
-                w[4 * i + 1] = u.y;
-                w[4 * i + 2] = u.z;
-                w[4 * i + 3] = u.w;
+                cp_async_zfill<16>(dst + 8 * i * GM_WSTRIDE, 8 * i < rows ? wsrc : p.qweight, 8 * i < rows ? 16 : 0);
             } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) w[4 * i + c] = valid && n + c < p.N ? (uint32_t)__ldg(src + n + c) : 0u;
+                for (int c = 0; c < 4; ++c) {
+                    const bool in = 8 * i < rows && left > c;
+                    cp_async_zfill<4>(dst + 8 * i * GM_WSTRIDE + 4 * c, in ? wsrc + c : p.qweight, in ? 4 : 0);
+                }
             }
+            wsrc += step8;
+        }
+        const int k = st * GM_K + 8 * lc;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int r = lr + 8 * i;
+            const bool in = m0 + r < p.M && k < K;
+            cp_async_zfill<8 * sizeof(XT)>(base + Cfg::W_BYTES + (uint32_t)(r * Cfg::XSTRIDE + lc * 8 * (int)sizeof(XT)),
+                                           in ? X + (long long)(m0 + r) * K + k : X, in ? 8 * sizeof(XT) : 0);
         }
     };
-    auto load_group = [&](long long gi) {
+
+    // ---- scales and zero points of this thread's rows n0 .. n0 + 3, one stage ahead, as loaded
+    const long long n0 = nc + 32 * nw + 4 * gid;
+    const long long zwords = (p.N * BITS + 31) / 32;
+    const int gmask = (int)((1u << p.gshift) - 1u);   // one group per row: no column but the first begins one
+    uint2 s_raw[GROUPS], s_next[GROUPS] = {};
+    constexpr int ZW = BITS == 3 ? 2 : 1;   // words that hold four zero points
+    uint32_t z_raw[GROUPS][ZW], z_next[GROUPS][ZW] = {};
+    auto load_group = [&](int gi, uint2& sr, uint32_t (&zr)[ZW]) {
+        const __half* sp = p.scales + (long long)gi * p.N + n0;
+        sr = make_uint2(0, 0);
+        if (p.vec) {
+            if (n0 < p.N) sr = __ldg(reinterpret_cast<const uint2*>(sp));
+        } else {
+            uint32_t h[4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const long long n = n0 + 32 * i;
-            if (p.vec) {
-                const uint2 u = n < p.N ? __ldg(reinterpret_cast<const uint2*>(p.scales + gi * p.N + n)) : make_uint2(0, 0);
-                const float2 a = __half22float2(as_half2(u.x)), b = __half22float2(as_half2(u.y));
-                sc[4 * i] = a.x;
-                sc[4 * i + 1] = a.y;
-                sc[4 * i + 2] = b.x;
-                sc[4 * i + 3] = b.y;
-            } else {
+            for (int c = 0; c < 4; ++c) h[c] = n0 + c < p.N ? __half_as_ushort(sp[c]) : 0u;
+            sr = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        }
+        // as loaded: the first use of a load waits for it.  n0 is a multiple of 4, so only 3-bit zero
+        // points straddle words.
+        if (p.qzeros != nullptr && n0 < p.N) {
+            const uint32_t* zp = reinterpret_cast<const uint32_t*>(p.qzeros) + gi * zwords + (n0 * BITS >> 5);
+            zr[0] = __ldg(zp);
+            if constexpr (ZW == 2) zr[ZW - 1] = __ldg(zp + ((n0 * BITS >> 5) + 1 < zwords ? 1 : 0));
+        }
+    };
+    // groups that begin in the 128 columns from k on (or the one that k lies in, at the run's start)
+    auto load_groups = [&](int k, bool start) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    sc[4 * i + c] = n + c < p.N ? __half2float(p.scales[gi * p.N + n + c]) : 0.f;
-            }
-            uint32_t z4 = 0;   // four zero points; n is a multiple of 4, so only 3-bit ones straddle words
-            if (p.qzeros != nullptr && n < p.N) {
-                const uint32_t* zp = reinterpret_cast<const uint32_t*>(p.qzeros) + gi * zwords;
-                const long long bit = n * BITS, k = bit >> 5;
-                z4 = __ldg(zp + k) >> (bit & 31);
-                if (BITS == 3 && (bit & 31) > 20 && k + 1 < zwords) z4 |= __ldg(zp + k + 1) << (32 - (bit & 31));
-            }
+        for (int i = 0; i < GROUPS; ++i) {
+            const int kk = k + (G16 ? 16 : 32) * i;
+            if (kk < K && (G16 || (kk & gmask) == 0 || (i == 0 && start))) load_group(kk >> p.gshift, s_next[i], z_next[i]);
+        }
+    };
+
+    float total[2][MT][4] = {}, part[2][MT][4] = {};   // tile j: rows n0 + j (first 8 of the tile) and n0 + j + 2
+    float sc[4] = {};
+    uint32_t zz[4] = {};
+    const uint32_t zshift = (uint32_t)(n0 * BITS) & 31u;
+    auto use_group = [&](const uint2& sr, const uint32_t (&zw)[ZW]) {
+        const uint32_t zr = ZW == 2 ? __funnelshift_r(zw[0], zw[ZW - 1], zshift) : zw[0] >> zshift;
+        const float2 a = __half22float2(as_half2(sr.x)), b = __half22float2(as_half2(sr.y));
+        sc[0] = a.x;
+        sc[1] = a.y;
+        sc[2] = b.x;
+        sc[3] = b.y;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t z = p.qzeros != nullptr ? (z4 >> (BITS * c)) & ((1u << BITS) - 1u) : 1u << (BITS - 1);
-                zz[4 * i + c] = zero_pair<BITS>(z, XT());
-            }
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t z = p.qzeros != nullptr ? (zr >> (BITS * c)) & ((1u << BITS) - 1u) : 1u << (BITS - 1);
+            zz[c] = zero_pair<BITS>(z, XT());
         }
     };
     auto flush = [&] {   // the group's sums, scaled
 #pragma unroll
-        for (int j = 0; j < TILES; ++j) {
-            const int lo = j, hi = NT == 2 ? 4 + j : j + 2;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                total[j][mt][0] = fmaf(sc[lo], part[j][mt][0], total[j][mt][0]);
-                total[j][mt][1] = fmaf(sc[lo], part[j][mt][1], total[j][mt][1]);
-                total[j][mt][2] = fmaf(sc[hi], part[j][mt][2], total[j][mt][2]);
-                total[j][mt][3] = fmaf(sc[hi], part[j][mt][3], total[j][mt][3]);
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) part[j][mt][c] = 0.f;
-            }
-        }
+                for (int c = 0; c < 4; ++c) {
+                    total[j][mt][c] = fmaf(sc[c < 2 ? j : j + 2], part[j][mt][c], total[j][mt][c]);
+                    part[j][mt][c] = 0.f;
+                }
     };
 
-    for (int u = u0; u < u1; ++u) {
-        uint32_t raw[4][WPC][4 * NT];
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {   // all of the unit's words first: their latencies overlap
-            const int k = u * GM_UNIT + 32 * st;
-            if constexpr (G16) {           // four codes of each half of the step
+    for (int i = 0; i < STAGES - 1; ++i) {
+        if (st0 + i < st1) issue(st0 + i);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    if (st0 < st1) load_groups(st0 * GM_K + 128 * kg, true);
+    for (int st = st0; st < st1; ++st) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        __syncthreads();   // the stage is complete, and everybody has left the one that is refilled
+        if (st + STAGES - 1 < st1) issue(st + STAGES - 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int kh = k + 16 * h + 4 * tig, sh = kh * BITS & 31;
-                    const long long r = (long long)kh * BITS / 32;
-                    load_row(r, kh < K, raw[st][h]);
-                    if constexpr (BITS == 3) load_row(r + 1, kh < K && sh > 20, raw[st][2 + h]);
-                }
-            } else {
-                const int kc = k + 8 * tig;
-                const long long r = (long long)kc * BITS / 32;
-                load_row(r, kc < K, raw[st][0]);
-                if constexpr (BITS == 8) load_row(r + 1, kc < K, raw[st][1]);
-                // codes of 24 bits that start past bit 8 of a word end in the next
-                if constexpr (BITS == 3) load_row(r + 1, kc < K && tig != 0 && tig != 3, raw[st][1]);
-            }
+        for (int i = 0; i < GROUPS; ++i) {
+            s_raw[i] = s_next[i];
+#pragma unroll
+            for (int j = 0; j < ZW; ++j) z_raw[i][j] = z_next[i][j];
         }
+        if (st + 1 < st1) load_groups(st * GM_K + 128 * kg + GM_K, false);
+
+        const uint8_t* base = gm_smem + (st - st0) % STAGES * Cfg::STAGE;
+        const uint8_t* wbase = base + kg * (Cfg::W_BYTES / 2) + (32 * nw + 4 * gid) * 4;
+        const uint8_t* xbase = base + Cfg::W_BYTES + gid * Cfg::XSTRIDE + 128 * kg * (int)sizeof(XT);
+        auto row = [&](int r) { return *reinterpret_cast<const uint4*>(wbase + r * GM_WSTRIDE); };
+        const int k0 = st * GM_K + 128 * kg;
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
-            const int k = u * GM_UNIT + 32 * st;
+        for (int s4 = 0; s4 < 4; ++s4) {
+            const int k = k0 + 32 * s4;
             if (k >= K) break;
-            if (!G16 && (k % p.g == 0 || (st == 0 && u == u0))) load_group(k / p.g);
+            if constexpr (!G16) {
+                if ((k & gmask) == 0 || (s4 == 0 && st == st0)) use_group(s_raw[s4], z_raw[s4]);
+            }
             uint32_t xb[MT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const int m = m0 + 8 * mt + gid;
-                xb[mt][0] = xb[mt][1] = xb[mt][2] = xb[mt][3] = 0u;
-                if constexpr (G16) {
-                    // columns k + 4 tig + 0 .. 3 and k + 16 + 4 tig + 0 .. 3
-                    if (m < p.M && k + 4 * tig < K) x_quad(X + (long long)m * K + k + 4 * tig, xb[mt][0], xb[mt][1]);
-                    if (m < p.M && k + 16 + 4 * tig < K)
-                        x_quad(X + (long long)m * K + k + 16 + 4 * tig, xb[mt][2], xb[mt][3]);
-                } else {
-                    if (m < p.M && k + 8 * tig < K) x_pairs(X + (long long)m * K + k + 8 * tig, xb[mt]);
-                }
+                const XT* x = reinterpret_cast<const XT*>(xbase + 8 * mt * Cfg::XSTRIDE) + 32 * s4;
+                if constexpr (G16)
+                    x_pairs<true>(load_x44(x + 4 * tig, x + 16 + 4 * tig), xb[mt]);
+                else
+                    x_pairs<false>(load_x8(x + 8 * tig), xb[mt]);
             }
+            if constexpr (!G16) {
+                uint4 w = row(s4 * BITS + (BITS == 8 ? 2 * tig : BITS == 4 ? tig : BITS == 2 ? tig >> 1 : 3 * tig >> 2));
+                uint4 w2 = w;
+                if constexpr (BITS == 8) w2 = row(s4 * BITS + 2 * tig + 1);
+                // 24 bits from bit 24 or 16 of a word on end in the next
+                if constexpr (BITS == 3) w2 = row(s4 * BITS + min((3 * tig >> 2) + 1, 2));
+                const uint32_t a0[4] = {w.x, w.y, w.z, w.w}, a1[4] = {w2.x, w2.y, w2.z, w2.w};
 #pragma unroll
-            for (int h = 0; h < (G16 ? 2 : 1); ++h) {
-                if constexpr (G16) {
-                    if (k + 16 * h >= K) break;
-                    load_group((k + 16 * h) / p.g);
-                }
-#pragma unroll
-                for (int j = 0; j < TILES; ++j) {
-                    const int lo = j, hi = NT == 2 ? 4 + j : j + 2;
-                    constexpr int NP = G16 ? 2 : 4;
-                    uint32_t a[NP], b[NP];   // rows gid and gid + 8 of the tile
-                    if constexpr (G16) {
-                        const int sh = (k + 16 * h + 4 * tig) * BITS & 31;
-                        uint32_t c, d;
-                        quad_nibbles<BITS>(raw[st][h][lo], raw[st][WPC - 2 + h][lo], sh, c, d);
-                        w_pairs<BITS, NP>(c, d, zz[lo], a, XT());
-                        quad_nibbles<BITS>(raw[st][h][hi], raw[st][WPC - 2 + h][hi], sh, c, d);
-                        w_pairs<BITS, NP>(c, d, zz[hi], b, XT());
-                    } else {
-                        const uint32_t l2 = raw[st][WPC - 1][lo], h2 = raw[st][WPC - 1][hi];
-                        w_pairs<BITS, NP>(chunk_nibbles<BITS>(raw[st][0][lo], l2, tig), l2, zz[lo], a, XT());
-                        w_pairs<BITS, NP>(chunk_nibbles<BITS>(raw[st][0][hi], h2, tig), h2, zz[hi], b, XT());
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t a[4], b[4];   // rows gid and gid + 8 of the tile
+                    w_pairs<BITS, 4>(chunk_nibbles<BITS>(a0[j], a1[j], tig), a1[j], zz[j], a, XT());
+                    w_pairs<BITS, 4>(chunk_nibbles<BITS>(a0[j + 2], a1[j + 2], tig), a1[j + 2], zz[j + 2], b, XT());
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        mma_16816(part[j][mt], a[0], b[0], a[1], b[1], xb[mt][2 * h], xb[mt][2 * h + 1], XT());
-                        if constexpr (!G16)
-                            mma_16816(part[j][mt], a[2], b[2], a[3], b[3], xb[mt][2], xb[mt][3], XT());
+                        mma_16816(part[j][mt], a[0], b[0], a[1], b[1], xb[mt][0], xb[mt][1], XT());
+                        mma_16816(part[j][mt], a[2], b[2], a[3], b[3], xb[mt][2], xb[mt][3], XT());
                     }
                 }
-                if (G16) flush();
+                if (p.gshift <= 7 && (((k + 32) & gmask) == 0 || k + 32 >= K)) flush();
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (k + 16 * h >= K) break;
+                    use_group(s_raw[2 * s4 + h], z_raw[2 * s4 + h]);
+                    const int bit = (32 * s4 + 16 * h + 4 * tig) * BITS;   // of the four codes, in this run of words
+                    const uint4 w = row(bit >> 5);
+                    uint4 w2 = w;
+                    if constexpr (BITS == 3) w2 = row(min((bit >> 5) + 1, 4 * BITS - 1));
+                    const uint32_t a0[4] = {w.x, w.y, w.z, w.w}, a1[4] = {w2.x, w2.y, w2.z, w2.w};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t c, d, a[2], b[2];
+                        quad_nibbles<BITS>(a0[j], a1[j], bit & 31, c, d);
+                        w_pairs<BITS, 2>(c, d, zz[j], a, XT());
+                        quad_nibbles<BITS>(a0[j + 2], a1[j + 2], bit & 31, c, d);
+                        w_pairs<BITS, 2>(c, d, zz[j + 2], b, XT());
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            mma_16816(part[j][mt], a[0], b[0], a[1], b[1], xb[mt][2 * h], xb[mt][2 * h + 1], XT());
+                    }
+                    flush();
+                }
             }
-            if (!G16 && ((k + 32) % p.g == 0 || k + 32 >= K || (st == 3 && u == u1 - 1))) flush();
         }
     }
+    if (p.gshift > 7) flush();   // one group per row
 
-    // join the warps' sums, then those of the cluster's CTAs, in a fixed order
-#pragma unroll
-    for (int j = 0; j < TILES; ++j) {
-        const int lo = 4 * gid + j, hi = NT == 2 ? 32 + 4 * gid + j : 4 * gid + j + 2;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int t = 8 * mt + 2 * tig;
-            red[warp][t][lo] = total[j][mt][0];
-            red[warp][t + 1][lo] = total[j][mt][1];
-            red[warp][t][hi] = total[j][mt][2];
-            red[warp][t + 1][hi] = total[j][mt][3];
-        }
-    }
+    // ---- join the two runs of columns, then the CTAs of the cluster, in a fixed order
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    const long long nc = (long long)(cta % p.nblocks) * ROWS;
+    float* sums = reinterpret_cast<float*>(gm_smem);   // [2][TOK][GM_ROWS]
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sums[(kg * TOK + 8 * mt + 2 * tig + (c & 1)) * GM_ROWS + 32 * nw + 4 * gid + j + (c & 2)] = total[j][mt][c];
+    __syncthreads();
     auto finish = [&](int e, float y) {
-        const int m = m0 + e / ROWS;
-        const long long n = nc + e % ROWS;
+        const int m = m0 + e / GM_ROWS;
+        const long long n = nc + e % GM_ROWS;
         if (m < p.M && n < p.N) store_y(p.Y, p.y_bf16, (long long)m * p.N + n, p.x_scale ? y * p.x_scale[m] : y);
     };
-    for (int e = threadIdx.x; e < TOK * ROWS; e += 32 * GM_WARPS) {
-        float y = 0.f;
-#pragma unroll
-        for (int w = 0; w < GM_WARPS; ++w) y += (&red[w][0][0])[e];
-        if (p.split == 1)
-            finish(e, y);
-        else
-            (&red[0][0][0])[e] = y;   // read above by this thread alone
-    }
-    if (p.split > 1) {
+    constexpr int E = TOK * GM_ROWS;
+    if (p.split == 1) {
+        for (int e = tid; e < E; e += GM_THREADS) finish(e, sums[e] + sums[E + e]);
+    } else {
         __syncwarp();
         cluster_sync_all();
-        for (int e = (int)rank * (32 * GM_WARPS) + threadIdx.x; e < TOK * ROWS; e += (int)p.split * (32 * GM_WARPS)) {
+        for (int e = (int)rank * GM_THREADS + tid; e < E; e += (int)p.split * GM_THREADS) {
             float y = 0.f;
-            for (unsigned r = 0; r < p.split; ++r) y += ld_cluster_f32(smem_u32(&red[0][0][0] + e), r);
+            for (unsigned r = 0; r < p.split; ++r)
+                y += ld_cluster_f32(smem_u32(sums + e), r) + ld_cluster_f32(smem_u32(sums + E + e), r);
             finish(e, y);
         }
         __syncwarp();
@@ -426,20 +505,31 @@ namespace gqh {
 
 int num_sms();
 
-template <int BITS, typename XT, int MT, int NT, bool G16>
+template <int BITS, typename XT, int MT, bool G16>
 cudaError_t gemv_mma_launch(gq::GemvArgs p, cudaStream_t st) {
-    constexpr int ROWS = 32 * NT, TOK = 8 * MT;
-    p.nblocks = (unsigned)((p.N + ROWS - 1) / ROWS);
+    using Cfg = gq::GmCfg<BITS, XT, MT>;
+    constexpr auto kern = gq::gemv_mma_kernel<BITS, XT, MT, G16>;
+    GQ_TRY((smem_attr_once<kern, Cfg::SMEM>()));
+    p.nblocks = (unsigned)((p.N + gq::GM_ROWS - 1) / gq::GM_ROWS);
     p.vec = p.N % 4 == 0;
-    const long long blocks = (long long)p.nblocks * ((p.M + TOK - 1) / TOK);
-    // K is split until two CTAs per SM have work, with a unit at least for each warp
-    p.split = 1;
-    while (p.split < 8 && blocks * p.split < 2 * num_sms() && p.K > (long long)gq::GM_UNIT * gq::GM_WARPS * p.split)
-        p.split *= 2;
+    p.gshift = p.g_all ? 31 : p.g == 128 ? 7 : p.g == 64 ? 6 : p.g == 32 ? 5 : 4;
+    const long long blocks = (long long)p.nblocks * ((p.M + Cfg::TOK - 1) / Cfg::TOK);
+    // K is split over a cluster where that shortens the run: waves of two CTAs to an SM, times the
+    // stages of a CTA and about one for its start and end.
+    const long long nst = (p.K + gq::GM_K - 1) / gq::GM_K, slots = 2ll * num_sms();
+    long long best = 0;
+    for (unsigned s = 1; s <= 8 && s <= nst; s *= 2) {
+        const long long cost = (blocks * s + slots - 1) / slots * ((nst + s - 1) / s + 1);
+        if (s == 1 || cost < best) {
+            best = cost;
+            p.split = s;
+        }
+    }
     if (blocks * p.split > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * p.split));
-    cfg.blockDim = dim3(32 * gq::GM_WARPS);
+    cfg.blockDim = dim3(gq::GM_THREADS);
+    cfg.dynamicSmemBytes = Cfg::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -447,17 +537,17 @@ cudaError_t gemv_mma_launch(gq::GemvArgs p, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gq::gemv_mma_kernel<BITS, XT, MT, NT, G16>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess) (void)cudaGetLastError();
     return e;
 }
 
 template <int BITS, typename XT>
 cudaError_t gemv_mma_run(const gq::GemvArgs& p, cudaStream_t st) {
-    if (p.g == 16) return gemv_mma_launch<BITS, XT, 2, 1, true>(p, st);
-    if (p.M <= 8) return gemv_mma_launch<BITS, XT, 1, 2, false>(p, st);
-    if (p.M <= 16) return gemv_mma_launch<BITS, XT, 2, 1, false>(p, st);
-    return gemv_mma_launch<BITS, XT, 4, 1, false>(p, st);
+    if (p.g == 16 && !p.g_all) return gemv_mma_launch<BITS, XT, 2, true>(p, st);
+    if (p.M <= 8) return gemv_mma_launch<BITS, XT, 1, false>(p, st);
+    if (p.M <= 16) return gemv_mma_launch<BITS, XT, 2, false>(p, st);
+    return gemv_mma_launch<BITS, XT, 4, false>(p, st);
 }
 
 template <typename XT>

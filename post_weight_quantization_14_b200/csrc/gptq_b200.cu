@@ -674,7 +674,8 @@ gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale
     p.M = (int)M;
     p.N = d_out;
     p.K = d_in;
-    p.g = cfg->group_size < 0 ? (int)d_in : cfg->group_size;
+    p.g_all = cfg->group_size < 0;
+    p.g = p.g_all ? (int)d_in : cfg->group_size;
     p.ng = (int)((d_in + p.g - 1) / p.g);
     p.bits = cfg->bits;
     cudaError_t e = gemv_run(p, xt == GPTQ_E4M3, (cudaStream_t)stream);

@@ -127,6 +127,8 @@ GEMV = [
     (4, 516, 1536, 8, 16, False, 0, "e4m3", "f32"),
     (4, 516, 1536, 3, 16, False, 0, "e4m3", "f32"),
     (4, 516, 1536, 2, 16, True, 0, "bf16", "f32"),
+    (3, 40, 384, 4, -1, False, 0, "bf16", "f32"),      # one group per row; the last columns fill half a stage
+    (20, 132, 4224, 3, -1, True, 0, "e4m3", "f32"),
     # activation order
     (1, 1, 8, 4, -1, False, 1, "bf16", "f32"),
     (1, 37, 64, 3, 16, False, 1, "bf16", "f32"),
