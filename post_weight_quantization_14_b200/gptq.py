@@ -353,22 +353,60 @@ def gptq_dequant_gemm(X: torch.Tensor, qweight, scales, qzeros, d_out: int, d_in
     return Y
 
 
-_DTYPES = {torch.bfloat16: GPTQ_BF16, torch.float32: GPTQ_F32, torch.float8_e4m3fn: GPTQ_E4M3}
+# The serving calls below are made once per layer and token, so their checks are kept short: a comparison
+# that passes costs a fraction of a microsecond, and the longer checks that name what is wrong run only
+# when one fails.
+
+_BF16_F32 = {torch.bfloat16: GPTQ_BF16, torch.float32: GPTQ_F32}
+_BF16_E4M3 = {torch.bfloat16: GPTQ_BF16, torch.float8_e4m3fn: GPTQ_E4M3}
 
 
-def _dtype(t: torch.Tensor, allowed: tuple, name: str) -> int:
-    if t.dtype not in allowed:
-        raise ValueError(f"{name} must be {' or '.join(str(d)[6:] for d in allowed)} (got {t.dtype})")
-    return _DTYPES[t.dtype]
+def _dtype(t: torch.Tensor, allowed: dict, name: str) -> int:
+    try:
+        return allowed[t.dtype]
+    except (KeyError, AttributeError):
+        raise ValueError(f"{name} must be a {' or '.join(str(d)[6:] for d in allowed)} tensor") from None
 
 
-def _ptrs(*tensors: torch.Tensor | None) -> list[int | None]:
-    """Addresses of contiguous tensors that all sit on the current CUDA device."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+def _shape(t: torch.Tensor, dtype, shape: tuple, name: str) -> None:
+    if t.shape != shape or t.dtype != dtype:
+        _need(t, dtype, shape, name)
+
+
+def _packed(cfg: GptqConfig, d_out: int, d_in: int, qweight, scales, qzeros) -> None:
+    """The packed arrays of a layer, as _quant_outputs checks them."""
+    bits, g = cfg.bits, cfg.group_size
+    ng = 1 if g == -1 else -(-d_in // g) if g > 0 else 0
+    try:
+        ok = (qweight.shape == ((d_in * bits + 31) // 32, d_out) and qweight.dtype in _WORD
+              and scales.shape == (ng, d_out) and scales.dtype == torch.float16
+              and (qzeros is None if cfg.sym else
+                   qzeros.shape == (ng, (d_out * bits + 31) // 32) and qzeros.dtype in _WORD))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _quant_outputs(cfg, d_out, d_in, qweight, scales, qzeros, None)
+
+
+def _addresses(stream, *tensors: torch.Tensor | None) -> tuple:
+    """The stream and the addresses of contiguous tensors, all of the current CUDA device."""
+    dev, out = -2, []
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
-    return [_ptr(t) for t in tensors]
+        if t is None:
+            out.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("tensor must be on a CUDA device")
+            current = torch.cuda.current_device()
+            if d != current:
+                raise ValueError(f"tensor on cuda:{d}, the current device is cuda:{current}")
+            dev = d
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        out.append(t.data_ptr())
+    return (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream, *out)
 
 
 def gptq_dequant_gemv(X: torch.Tensor, qweight, scales, qzeros, d_out: int, d_in: int, cfg: GptqConfig,
@@ -377,24 +415,26 @@ def gptq_dequant_gemv(X: torch.Tensor, qweight, scales, qzeros, d_out: int, d_in
     """Y = X W_hat^T for up to GPTQ_GEMV_MAX_M rows, from any packed layout.  X: bfloat16 [M, d_in], or
     float8_e4m3fn with x_scale float32 [M]; Y: bfloat16 or float32 [M, d_out]; g_idx: int32 [d_in] iff
     cfg.desc_act."""
-    xt = _dtype(X, (torch.bfloat16, torch.float8_e4m3fn), "X")
-    yt = _dtype(Y, (torch.bfloat16, torch.float32), "Y")
+    xt = _dtype(X, _BF16_E4M3, "X")
+    yt = _dtype(Y, _BF16_F32, "Y")
     if X.dim() != 2:
         raise ValueError("X must be a [M, d_in] matrix")
     M = X.shape[0]
-    _need(X, X.dtype, (M, d_in), "X")
-    _need(Y, Y.dtype, (M, d_out), "Y")
-    _quant_outputs(cfg, d_out, d_in, qweight, scales, qzeros, None)
+    _shape(X, X.dtype, (M, d_in), "X")
+    _shape(Y, Y.dtype, (M, d_out), "Y")
+    _packed(cfg, d_out, d_in, qweight, scales, qzeros)
     if (x_scale is not None) != (xt == GPTQ_E4M3):
         raise ValueError("x_scale must be given iff X is float8_e4m3fn")
     if x_scale is not None:
-        _need(x_scale, torch.float32, (M,), "x_scale")
+        _shape(x_scale, torch.float32, (M,), "x_scale")
     if (g_idx is not None) != (cfg.desc_act != 0):
         raise ValueError("g_idx must be given iff cfg.desc_act is not 0")
     if g_idx is not None:
-        _need(g_idx, torch.int32, (d_in,), "g_idx")
-    x, xs, w, s, z, gi, y = _ptrs(X, x_scale, qweight, scales, qzeros, g_idx, Y)
-    _check(lib().gptq_dequant_gemv(x, xt, xs, M, w, s, z, gi, d_out, d_in, ctypes.byref(cfg), y, yt, _stream(stream)))
+        _shape(g_idx, torch.int32, (d_in,), "g_idx")
+    st, x, xs, w, s, z, gi, y = _addresses(stream, X, x_scale, qweight, scales, qzeros, g_idx, Y)
+    status = (_lib or lib()).gptq_dequant_gemv(x, xt, xs, M, w, s, z, gi, d_out, d_in, ctypes.byref(cfg), y, yt, st)
+    if status:
+        _check(status)
     return Y
 
 
@@ -404,49 +444,55 @@ def gptq_rms_norm_e4m3(X: torch.Tensor, weight: torch.Tensor, X8: torch.Tensor, 
     """Root-mean-square norm of X + residual to float8_e4m3fn rows X8 with float32 scales x_scale [M];
     residual_out receives X + residual (it may be residual or X).  X, residual: bfloat16 or float32
     [M, d_in]; weight: bfloat16 or float32 [d_in]."""
-    xt = _dtype(X, (torch.bfloat16, torch.float32), "X")
-    wt = _dtype(weight, (torch.bfloat16, torch.float32), "weight")
+    xt = _dtype(X, _BF16_F32, "X")
+    wt = _dtype(weight, _BF16_F32, "weight")
     if X.dim() != 2:
         raise ValueError("X must be a [M, d_in] matrix")
     M, d_in = X.shape
-    _need(weight, weight.dtype, (d_in,), "weight")
-    _need(X8, torch.float8_e4m3fn, (M, d_in), "X8")
-    _need(x_scale, torch.float32, (M,), "x_scale")
+    _shape(weight, weight.dtype, (d_in,), "weight")
+    _shape(X8, torch.float8_e4m3fn, (M, d_in), "X8")
+    _shape(x_scale, torch.float32, (M,), "x_scale")
     if (residual is None) != (residual_out is None):
         raise ValueError("residual and residual_out must be given together")
     if residual is not None:
-        _need(residual, X.dtype, (M, d_in), "residual")
-        _need(residual_out, X.dtype, (M, d_in), "residual_out")
-    x, r, w, x8, xs, r2 = _ptrs(X, residual, weight, X8, x_scale, residual_out)
-    _check(lib().gptq_rms_norm_e4m3(x, r, xt, w, wt, M, d_in, eps, x8, xs, r2, _stream(stream)))
+        _shape(residual, X.dtype, (M, d_in), "residual")
+        _shape(residual_out, X.dtype, (M, d_in), "residual_out")
+    st, x, r, w, x8, xs, r2 = _addresses(stream, X, residual, weight, X8, x_scale, residual_out)
+    status = (_lib or lib()).gptq_rms_norm_e4m3(x, r, xt, w, wt, M, d_in, eps, x8, xs, r2, st)
+    if status:
+        _check(status)
 
 
 def gptq_quantize_e4m3(X: torch.Tensor, X8: torch.Tensor, x_scale: torch.Tensor, stream=None) -> None:
     """Rows of X (bfloat16 or float32 [M, d_in]) to float8_e4m3fn X8 with float32 scales x_scale [M]."""
-    xt = _dtype(X, (torch.bfloat16, torch.float32), "X")
+    xt = _dtype(X, _BF16_F32, "X")
     if X.dim() != 2:
         raise ValueError("X must be a [M, d_in] matrix")
     M, d_in = X.shape
-    _need(X8, torch.float8_e4m3fn, (M, d_in), "X8")
-    _need(x_scale, torch.float32, (M,), "x_scale")
-    x, x8, xs = _ptrs(X, X8, x_scale)
-    _check(lib().gptq_quantize_e4m3(x, xt, M, d_in, x8, xs, _stream(stream)))
+    _shape(X8, torch.float8_e4m3fn, (M, d_in), "X8")
+    _shape(x_scale, torch.float32, (M,), "x_scale")
+    st, x, x8, xs = _addresses(stream, X, X8, x_scale)
+    status = (_lib or lib()).gptq_quantize_e4m3(x, xt, M, d_in, x8, xs, st)
+    if status:
+        _check(status)
 
 
 def gptq_dequant_gemm_e4m3(X8: torch.Tensor, x_scale: torch.Tensor, qweight, scales, qzeros, d_out: int, d_in: int,
                            cfg: GptqConfig, Y: torch.Tensor, stream=None) -> torch.Tensor:
     """Y = diag(x_scale) X8 W_hat^T from the packed arrays.  X8: float8_e4m3fn [M, d_in]; x_scale: float32
     [M]; Y: bfloat16 or float32 [M, d_out]."""
-    yt = _dtype(Y, (torch.bfloat16, torch.float32), "Y")
+    yt = _dtype(Y, _BF16_F32, "Y")
     if X8.dim() != 2:
         raise ValueError("X8 must be a [M, d_in] matrix")
     M = X8.shape[0]
-    _need(X8, torch.float8_e4m3fn, (M, d_in), "X8")
-    _need(x_scale, torch.float32, (M,), "x_scale")
-    _need(Y, Y.dtype, (M, d_out), "Y")
-    _quant_outputs(cfg, d_out, d_in, qweight, scales, qzeros, None)
-    x, xs, w, s, z, y = _ptrs(X8, x_scale, qweight, scales, qzeros, Y)
-    _check(lib().gptq_dequant_gemm_e4m3(x, xs, M, w, s, z, d_out, d_in, ctypes.byref(cfg), y, yt, _stream(stream)))
+    _shape(X8, torch.float8_e4m3fn, (M, d_in), "X8")
+    _shape(x_scale, torch.float32, (M,), "x_scale")
+    _shape(Y, Y.dtype, (M, d_out), "Y")
+    _packed(cfg, d_out, d_in, qweight, scales, qzeros)
+    st, x, xs, w, s, z, y = _addresses(stream, X8, x_scale, qweight, scales, qzeros, Y)
+    status = (_lib or lib()).gptq_dequant_gemm_e4m3(x, xs, M, w, s, z, d_out, d_in, ctypes.byref(cfg), y, yt, st)
+    if status:
+        _check(status)
     return Y
 
 
