@@ -706,7 +706,7 @@ gptq_status gptq_rms_norm_e4m3(const void* X, const void* residual, gptq_dtype x
     if (!aligned16(weight) || !aligned16(residual) || !aligned16(residual_out))
         return fail(GPTQ_ERR_INVALID_ARG, "weight, residual and residual_out must be 16-byte aligned");
     if (!(eps >= 0.f) || eps > 1e30f) return fail(GPTQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
-    const gq::RowsArgs p{X, residual, weight, X8, x_scale, residual_out, d_in, eps};
+    const gq::RowsArgs p{X, residual, weight, X8, x_scale, residual_out, d_in, M, eps, 0};
     cudaStream_t st = (cudaStream_t)stream;
     const char* name = "rms_norm_e4m3";
     cudaError_t e;
@@ -724,7 +724,7 @@ gptq_status gptq_quantize_e4m3(const void* X, gptq_dtype xt, int64_t M, int64_t 
                                void* stream) {
     gptq_status cs = check_rows(X, xt, M, d_in, X8, x_scale);
     if (cs != GPTQ_OK) return cs;
-    const gq::RowsArgs p{X, nullptr, nullptr, X8, x_scale, nullptr, d_in, 0.f};
+    const gq::RowsArgs p{X, nullptr, nullptr, X8, x_scale, nullptr, d_in, M, 0.f, 0};
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = xt == GPTQ_BF16 ? rows_e4m3_run<__nv_bfloat16, float, false>(p, M, "quantize_e4m3", st)
                                     : rows_e4m3_run<float, float, false>(p, M, "quantize_e4m3", st);

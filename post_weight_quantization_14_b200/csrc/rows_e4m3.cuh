@@ -12,6 +12,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace gq {
@@ -23,24 +25,41 @@ struct RowsArgs {
     uint8_t* X8;         // [M, D]
     float* x_scale;      // [M]
     void* R2;            // [M, D], with R
-    long long D;
+    long long D, M;
     float eps;
+    int warp_rows;       // a warp per row, not a CTA
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// Eight elements as loaded, so that a thread's loads can all be in flight before the first is used.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool valid) {
+        u = make_uint4(0, 0, 0, 0);
+        if (valid) u = *reinterpret_cast<const uint4*>(p);
     }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+    __device__ __forceinline__ float at(int i) const {
+        const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
+        return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);
+    }
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p, bool valid) {
+        a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (valid) {
+            a = *reinterpret_cast<const float4*>(p);
+            b = *reinterpret_cast<const float4*>(p + 4);
+        }
+    }
+    __device__ __forceinline__ float at(int i) const {
+        const float4 q = i < 4 ? a : b;
+        return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+    }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -68,23 +87,135 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float f, float inv)
     return make_uint2(r[0], r[1]);
 }
 
-constexpr int RW_THREADS = 256;
+// Joins the threads' sums and maxima over the warp or the block (up to 1024 threads), the same bits on
+// every run.
+template <bool NORM>
+__device__ __forceinline__ void rows_join(float& sum, uint32_t& top, bool warp_only) {
+    __shared__ float s_sum[32];
+    __shared__ uint32_t s_max[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        if (NORM) sum += __shfl_xor_sync(~0u, sum, o);
+        top = max(top, __shfl_xor_sync(~0u, top, o));
+    }
+    if (warp_only || warps == 1) return;
+    if (lane == 0) {
+        s_sum[warp] = sum;
+        s_max[warp] = top;
+    }
+    __syncthreads();
+    sum = lane < warps ? s_sum[lane] : 0.f;
+    top = lane < warps ? s_max[lane] : 0u;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        if (NORM) sum += __shfl_xor_sync(~0u, sum, o);
+        top = max(top, __shfl_xor_sync(~0u, top, o));
+    }
+}
 
-// One CTA per row, the row read twice.  A residual sum is read back from R' unless R' would
-// lose its low bits, so both passes form h from X and R; R' is written in the second pass, when
-// every element's own X and R have been read by the thread that writes it.
+struct RowScale {
+    float f, inv;   // X8 = e4m3((v f) inv)
+};
+template <bool NORM>
+__device__ __forceinline__ RowScale row_scale(const RowsArgs& p, float sum, uint32_t top, float* x_scale, bool first) {
+    const float a = __uint_as_float(top);
+    if (first) {
+        const float r = NORM ? rsqrtf(sum / (float)p.D + p.eps) : 1.f;
+        *x_scale = a == 0.f ? 0.f : r * (a / 448.f);
+    }
+    // a below 2^-100 would overflow 448 / a: the row is lifted by 2^64 first, which is exact
+    RowScale s;
+    s.f = a < 0x1p-100f ? 0x1p64f : 1.f;
+    s.inv = a > 0.f ? 448.f / (a * s.f) : (a == 0.f ? 0.f : a);
+    return s;
+}
+
+constexpr int RW_MAX_VECS = 4096;   // vectors of 8 elements in a row of rows_e4m3_kernel, at most
+// Threads of a CTA, at most, where a thread holds VEC vectors: 64 or 128 registers each.
+__host__ __device__ constexpr int rw_max_threads(int vec) { return vec <= 2 ? 1024 : 512; }
+
+// One CTA (or, for short rows, one warp) per row, the row in registers: VEC vectors of 8 elements a thread, so that X, R and w are read
+// once, all loads of a thread are in flight together, and R' is written before the maximum is known.
+// R' may be X or R: a thread writes only elements that it has read itself.
+template <typename XT, typename WT, bool NORM, int VEC>
+__global__ void __launch_bounds__(rw_max_threads(VEC)) rows_e4m3_kernel(const RowsArgs p) {
+    pdl_wait();
+    const bool wr = p.warp_rows != 0;
+    const long long row = wr ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= p.M) return;   // whole warps
+    const int t = wr ? threadIdx.x & 31 : threadIdx.x;
+    const XT* X = reinterpret_cast<const XT*>(p.X) + row * p.D;
+    const XT* R = p.R ? reinterpret_cast<const XT*>(p.R) + row * p.D : nullptr;
+    const int D = (int)p.D, step = wr ? 8 * 32 : 8 * (int)blockDim.x, c0 = 8 * t;
+    float v[VEC][8];
+    float sum = 0.f;
+    uint32_t top = 0;
+    constexpr int FLIGHT = VEC > 4 ? 4 : VEC;   // vectors of each input in flight
+#pragma unroll
+    for (int i0 = 0; i0 < VEC; i0 += FLIGHT) {
+        Raw8<XT> x[FLIGHT], r[FLIGHT];
+        Raw8<WT> w[FLIGHT];
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) x[i].load(X + c0 + (i0 + i) * step, c0 + (i0 + i) * step < D);
+        if (R) {
+#pragma unroll
+            for (int i = 0; i < FLIGHT; ++i) r[i].load(R + c0 + (i0 + i) * step, c0 + (i0 + i) * step < D);
+        }
+        if (NORM) {
+#pragma unroll
+            for (int i = 0; i < FLIGHT; ++i)
+                w[i].load(reinterpret_cast<const WT*>(p.w) + c0 + (i0 + i) * step, c0 + (i0 + i) * step < D);
+        }
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) {
+            float(&h)[8] = v[i0 + i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = x[i].at(j);
+            if (R) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[j] += r[i].at(j);
+                if (c0 + (i0 + i) * step < D) store8(reinterpret_cast<XT*>(p.R2) + row * p.D + c0 + (i0 + i) * step, h);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (NORM) {
+                    sum = fmaf(h[j], h[j], sum);
+                    h[j] *= w[i].at(j);
+                }
+                top = max(top, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+            }
+        }
+    }
+    rows_join<NORM>(sum, top, wr);
+    const RowScale s = row_scale<NORM>(p, sum, top, p.x_scale + row, t == 0);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const int c = c0 + i * step;
+        if (c < D) *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(v[i], s.f, s.inv);
+    }
+}
+
+// Rows too long for that: read twice, R' written in the second pass, when the thread that writes an
+// element has read its X and R.
 template <typename XT, typename WT, bool NORM>
-__global__ void __launch_bounds__(RW_THREADS) rows_e4m3_kernel(const RowsArgs p) {
-    __shared__ float s_sum[RW_THREADS / 32];
-    __shared__ uint32_t s_max[RW_THREADS / 32];
+__global__ void __launch_bounds__(1024) rows_e4m3_long_kernel(const RowsArgs p) {
+    pdl_wait();
     const long long row = blockIdx.x;
     const XT* X = reinterpret_cast<const XT*>(p.X) + row * p.D;
     const XT* R = p.R ? reinterpret_cast<const XT*>(p.R) + row * p.D : nullptr;
     const WT* W = reinterpret_cast<const WT*>(p.w);
+    const int D = (int)p.D, step = 8 * (int)blockDim.x;
     float sum = 0.f;
     uint32_t top = 0;
     float h[8], w[8];
-    auto read = [&](long long c) {
+    auto load8 = [](const auto* q, float (&to)[8]) {
+        Raw8<std::remove_cv_t<std::remove_pointer_t<decltype(q)>>> raw;
+        raw.load(q, true);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) to[i] = raw.at(i);
+    };
+    auto read = [&](int c) {
         load8(X + c, h);
         if (R) {
             load8(R + c, w);
@@ -92,7 +223,7 @@ __global__ void __launch_bounds__(RW_THREADS) rows_e4m3_kernel(const RowsArgs p)
             for (int i = 0; i < 8; ++i) h[i] += w[i];
         }
     };
-    for (long long c = 8ll * threadIdx.x; c < p.D; c += 8 * RW_THREADS) {
+    for (int c = 8 * (int)threadIdx.x; c < D; c += step) {
         read(c);
         if (NORM) load8(W + c, w);
 #pragma unroll
@@ -101,32 +232,9 @@ __global__ void __launch_bounds__(RW_THREADS) rows_e4m3_kernel(const RowsArgs p)
             top = max(top, __float_as_uint(NORM ? h[i] * w[i] : h[i]) & 0x7FFFFFFFu);
         }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        sum += __shfl_xor_sync(~0u, sum, o);
-        top = max(top, __shfl_xor_sync(~0u, top, o));
-    }
-    if ((threadIdx.x & 31) == 0) {
-        s_sum[threadIdx.x >> 5] = sum;
-        s_max[threadIdx.x >> 5] = top;
-    }
-    __syncthreads();
-    sum = 0.f;
-    top = 0;
-#pragma unroll
-    for (int i = 0; i < RW_THREADS / 32; ++i) {
-        sum += s_sum[i];
-        top = max(top, s_max[i]);
-    }
-    const float a = __uint_as_float(top);
-    // a below 2^-100 would overflow 448 / a: the row is lifted by 2^64 first, which is exact
-    const float f = a < 0x1p-100f ? 0x1p64f : 1.f;
-    const float inv = a > 0.f ? 448.f / (a * f) : (a == 0.f ? 0.f : a);
-    if (threadIdx.x == 0) {
-        const float r = NORM ? rsqrtf(sum / (float)p.D + p.eps) : 1.f;
-        p.x_scale[row] = a == 0.f ? 0.f : r * (a / 448.f);
-    }
-    for (long long c = 8ll * threadIdx.x; c < p.D; c += 8 * RW_THREADS) {
+    rows_join<NORM>(sum, top, false);
+    const RowScale s = row_scale<NORM>(p, sum, top, p.x_scale + row, threadIdx.x == 0);
+    for (int c = 8 * (int)threadIdx.x; c < D; c += step) {
         read(c);
         if (R) store8(reinterpret_cast<XT*>(p.R2) + row * p.D + c, h);
         if (NORM) {
@@ -134,7 +242,7 @@ __global__ void __launch_bounds__(RW_THREADS) rows_e4m3_kernel(const RowsArgs p)
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[i] *= w[i];
         }
-        *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(h, f, inv);
+        *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(h, s.f, s.inv);
     }
 }
 
@@ -142,10 +250,33 @@ __global__ void __launch_bounds__(RW_THREADS) rows_e4m3_kernel(const RowsArgs p)
 
 namespace gqh {
 
+int num_sms();
+
 template <typename XT, typename WT, bool NORM>
-cudaError_t rows_e4m3_run(const gq::RowsArgs& p, long long M, const char* name, cudaStream_t st) {
+cudaError_t rows_e4m3_run(gq::RowsArgs p, long long M, const char* name, cudaStream_t st) {
     TimedScope ts__(name, st);
-    return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM>, dim3((unsigned)M), dim3(gq::RW_THREADS), 0, st, p);
+    dim3 grid((unsigned)M);
+    const int vecs = (int)(p.D / 8);
+    p.M = M;
+    if (vecs > gq::RW_MAX_VECS)
+        return launch_pdl(gq::rows_e4m3_long_kernel<XT, WT, NORM>, grid, dim3(1024), 0, st, p);
+    // Few rows: a vector a thread, for latency.  Many rows: four, for bytes in flight and cheap barriers.
+    const bool few = M <= 2 * num_sms();
+    int vec = few ? 1 : 4, threads;
+    while (vec * gq::rw_max_threads(vec) < vecs) vec *= 2;
+    threads = ((vecs + vec - 1) / vec + 31) / 32 * 32;
+    p.warp_rows = !few && threads == 32;   // short rows: eight to a CTA, which starts as fast as one row's
+    if (p.warp_rows) {
+        while (vec > 1 && vec * 16 >= vecs) vec /= 2;
+        threads = 256;
+        grid.x = (unsigned)((M + 7) / 8);
+    }
+    switch (vec) {
+        case 1: return launch_pdl(gq::rows_e4m3_kernel<XT, WT, NORM, 1>, grid, dim3(threads), 0, st, p);
+        case 2: return launch_pdl(gq::rows_e4m3_kernel<XT, WT, NORM, 2>, grid, dim3(threads), 0, st, p);
+        case 4: return launch_pdl(gq::rows_e4m3_kernel<XT, WT, NORM, 4>, grid, dim3(threads), 0, st, p);
+        default: return launch_pdl(gq::rows_e4m3_kernel<XT, WT, NORM, 8>, grid, dim3(threads), 0, st, p);
+    }
 }
 
 }  // namespace gqh
