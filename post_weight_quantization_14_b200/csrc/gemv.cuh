@@ -5,7 +5,7 @@
 // with g(k) = k / g, or g_idx[k] for layers quantized in activation order.  X is bf16 (xs = 1)
 // or e4m3 with one fp32 scale per row.
 //
-// Two kernels:
+// Three kernels:
 //
 // gemv_mma_kernel (groups of consecutive columns).  The work is one pass over the packed words, so
 // the design is about issue slots next to the loads: with fp32 FMAs every weight costs an unpack, a
@@ -21,8 +21,8 @@
 // take 32 rows each of a stage's first 128 columns, four of the others.  The halves' sums, and those of
 // the CTAs of a cluster that split K, are joined in a fixed order through shared memory.
 //
-// gemv_lane_kernel (g_idx, any column in any group).  One lane per row n; eight warps split the
-// columns.  s (q - z) (at most 11 + 8 significant bits) is exact in fp32.
+// gemv_act_kernel (g_idx: any column in any group; see there), and gemv_lane_kernel for layers with so
+// many groups that its table does not fit: one lane per row n, eight warps split the columns.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -154,6 +154,24 @@ __device__ __forceinline__ XRaw<__nv_bfloat16> load_x44(const __nv_bfloat16* lo,
 }
 __device__ __forceinline__ XRaw<__nv_fp8_e4m3> load_x44(const __nv_fp8_e4m3* lo, const __nv_fp8_e4m3* hi) {
     return {make_uint2(*reinterpret_cast<const uint32_t*>(lo), *reinterpret_cast<const uint32_t*>(hi))};
+}
+__device__ __forceinline__ void x_floats(const XRaw<__nv_bfloat16>& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void x_floats(const XRaw<__nv_fp8_e4m3>& r, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = (i < 2 ? r.u.x : r.u.y) >> (16 * (i & 1));
+        const float2 f = __half22float2(
+            __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3)));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
 }
 // The columns in pairs: (i, i + 4), i = 0 .. 3; or (0, 2), (1, 3) of the first four and of the second.
 template <bool G16>
@@ -499,6 +517,158 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
     }
 }
 
+// Activation order: any column in any group.  The work is a lookup of a scale and a zero point for every
+// weight, so the CTA keeps those of all groups for its rows n in shared memory, as (scale, 1024 + zero
+// point) in fp16, and a lane's 4 (or, where there are too many groups for that, 1) rows are neighbours:
+// one read gives a column's entries for them, and the packed words are read along n.  A warp takes
+// chunks of 8 columns; the 8 warps of a CTA and the CTAs of a cluster split K.  s (q - z) (at most
+// 11 + 8 significant bits) is exact in fp32, and sums are fp32.
+constexpr int GA_THREADS = 256;
+constexpr int GA_TABLE = 160 * 1024;   // bytes of the table, at most
+
+template <int BITS, typename XT, int TM, int NL>
+__global__ void __launch_bounds__(GA_THREADS) gemv_act_kernel(const GemvArgs p) {
+    constexpr int ROWS = 32 * NL;
+    extern __shared__ __align__(16) uint8_t ga_smem[];
+    __half2* table = reinterpret_cast<__half2*>(ga_smem);   // [ng][ROWS]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const unsigned cta = blockIdx.x / p.split, rank = blockIdx.x % p.split;
+    const long long nc = (long long)(cta % p.nblocks) * ROWS, n0 = nc + NL * lane;
+    const int m0 = (int)(cta / p.nblocks) * TM;
+    const int K = (int)p.K, chunks = K / 8;
+    const XT* X = reinterpret_cast<const XT*>(p.X);
+    const long long zwords = (p.N * BITS + 31) / 32;
+
+    for (int e = tid; e < p.ng * ROWS; e += GA_THREADS) {
+        const int gi = e / ROWS;
+        const long long n = nc + e % ROWS;
+        __half s = __float2half(0.f);
+        uint32_t z = 1u << (BITS - 1);
+        if (n < p.N) {
+            s = p.scales[(long long)gi * p.N + n];
+            if (p.qzeros != nullptr) z = stream_code(p.qzeros + gi * zwords, 1, n, BITS);
+        }
+        table[e] = __halves2half2(s, __ushort_as_half((unsigned short)(0x6400u | z)));   // 1024 + z
+    }
+    __syncthreads();
+
+    // chunks of this CTA, taken by its warps in turn
+    const int c0 = (int)((long long)chunks * rank / p.split), c1 = (int)((long long)chunks * (rank + 1) / p.split);
+    struct Chunk {
+        uint32_t w[2][NL];
+        int4 g[2];
+        XRaw<XT> x[TM];
+    };
+    auto load = [&](int c, Chunk& q) {
+        const int k = 8 * c;
+        const long long r = (long long)k * BITS / 32;
+        // 24 bits from bit 16 or 24 of a word on end in the next
+        const int words = BITS == 8 || (BITS == 3 && ((k * 3) & 31) > 8) ? 2 : 1;
+#pragma unroll
+        for (int i = 0; i < (BITS == 8 || BITS == 3 ? 2 : 1); ++i) {
+            const int32_t* src = p.qweight + (r + (i < words ? i : 0)) * p.N + n0;
+            if (NL == 4 && p.vec) {
+                const uint4 u = n0 < p.N ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+                q.w[i][0] = u.x;
+                q.w[i][1 % NL] = u.y;
+                q.w[i][2 % NL] = u.z;
+                q.w[i][3 % NL] = u.w;
+                if (NL == 1) q.w[i][0] = u.x;
+            } else {
+#pragma unroll
+                for (int j = 0; j < NL; ++j) q.w[i][j] = n0 + j < p.N ? (uint32_t)__ldg(src + j) : 0u;
+            }
+        }
+        if constexpr (BITS < 8 && BITS != 3) {
+#pragma unroll
+            for (int j = 0; j < NL; ++j) q.w[1][j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) reinterpret_cast<int*>(q.g)[j] = __ldg(p.g_idx + k + j);
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+            if (m0 + t < p.M) q.x[t] = load_x8(X + (long long)(m0 + t) * K + k);
+    };
+    float acc[TM][NL] = {};
+    Chunk now = {}, next = {};
+    int c = c0 + warp;
+    if (c < c1) load(c, now);
+    for (; c < c1; c += GA_THREADS / 32) {
+        if (c + GA_THREADS / 32 < c1) load(c + GA_THREADS / 32, next);
+        uint32_t nib[NL];
+        if constexpr (BITS <= 4) {
+#pragma unroll
+            for (int j = 0; j < NL; ++j) nib[j] = chunk_nibbles<BITS>(now.w[0][j], now.w[1][j], c & 3);
+        }
+        float x[TM][8];
+#pragma unroll
+        for (int t = 0; t < TM; ++t) x_floats(now.x[t], x[t]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int gi = reinterpret_cast<const int*>(now.g)[i];
+            if ((unsigned)gi >= (unsigned)p.ng) {
+                if (lane == 0) record_status(GPTQ_ERR_INVALID_ARG, 8ll * c + i);
+                gi = 0;
+            }
+            uint32_t e[NL];
+            if constexpr (NL == 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(table + gi * ROWS + 4 * lane);
+                e[0] = u.x;
+                e[1] = u.y;
+                e[2] = u.z;
+                e[3] = u.w;
+            } else {
+                e[0] = *reinterpret_cast<const uint32_t*>(table + gi * ROWS + lane);
+            }
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const uint32_t q = BITS <= 4 ? (nib[j] >> (4 * i)) & 15u : (now.w[i >> 2][j] >> (8 * (i & 3))) & 255u;
+                const float2 sz = __half22float2(as_half2(e[j]));
+                // 0x44800000 | q << 13 is 1024 + q
+                const float w = sz.x * (__uint_as_float(0x44800000u | (q << 13)) - sz.y);
+#pragma unroll
+                for (int t = 0; t < TM; ++t) acc[t][j] = fmaf(x[t][i], w, acc[t][j]);
+            }
+        }
+        now = next;
+    }
+
+    // join the warps, then the CTAs of the cluster, in a fixed order
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ga_smem);   // [8 warps][TM][ROWS]
+    constexpr int E = TM * ROWS;
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+        for (int j = 0; j < NL; ++j) sums[warp * E + t * ROWS + NL * lane + j] = acc[t][j];
+    __syncthreads();
+    auto finish = [&](int e, float y) {
+        const int m = m0 + e / ROWS;
+        const long long n = nc + e % ROWS;
+        if (m < p.M && n < p.N) store_y(p.Y, p.y_bf16, (long long)m * p.N + n, p.x_scale ? y * p.x_scale[m] : y);
+    };
+    for (int e = tid; e < E; e += GA_THREADS) {
+        float y = 0.f;
+#pragma unroll
+        for (int w = 0; w < GA_THREADS / 32; ++w) y += sums[w * E + e];
+        if (p.split == 1)
+            finish(e, y);
+        else
+            sums[e] = y;   // read above by this thread alone
+    }
+    if (p.split > 1) {
+        __syncwarp();
+        cluster_sync_all();
+        for (int e = (int)rank * GA_THREADS + tid; e < E; e += (int)p.split * GA_THREADS) {
+            float y = 0.f;
+            for (unsigned r = 0; r < p.split; ++r) y += ld_cluster_f32(smem_u32(sums + e), r);
+            finish(e, y);
+        }
+        __syncwarp();
+        cluster_sync_all();   // no CTA leaves while its sums are being read
+    }
+}
+
 }  // namespace gq
 
 namespace gqh {
@@ -550,6 +720,46 @@ cudaError_t gemv_mma_run(const gq::GemvArgs& p, cudaStream_t st) {
     return gemv_mma_launch<BITS, XT, 4, false>(p, st);
 }
 
+template <int BITS, typename XT, int TM, int NL>
+cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
+    constexpr int ROWS = 32 * NL;
+    constexpr auto kern = gq::gemv_act_kernel<BITS, XT, TM, NL>;
+    GQ_TRY((smem_attr_once<kern, gq::GA_TABLE>()));
+    p.nblocks = (unsigned)((p.N + ROWS - 1) / ROWS);
+    p.vec = p.N % 4 == 0;
+    const long long blocks = (long long)p.nblocks * ((p.M + TM - 1) / TM);
+    // K is split until there are two CTAs to an SM, with four chunks at least for each warp
+    p.split = 1;
+    while (p.split < 8 && blocks * p.split < 2 * num_sms() && p.K >= 8ll * 32 * 2 * p.split) p.split *= 2;
+    if (blocks * p.split > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * p.split));
+    cfg.blockDim = dim3(gq::GA_THREADS);
+    cfg.dynamicSmemBytes = std::max((size_t)p.ng * ROWS * 4, (size_t)(gq::GA_THREADS / 32) * TM * ROWS * 4);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
+}
+
+// True where the table of gemv_act_kernel fits; the launch's status is then in *e.
+template <int BITS, typename XT>
+bool gemv_act_run(const gq::GemvArgs& p, cudaStream_t st, cudaError_t* e) {
+    if ((long long)p.ng * 128 * 4 <= gq::GA_TABLE)
+        *e = p.M <= 2 ? gemv_act_launch<BITS, XT, 2, 4>(p, st) : gemv_act_launch<BITS, XT, 8, 4>(p, st);
+    else if ((long long)p.ng * 32 * 4 <= gq::GA_TABLE)
+        *e = p.M <= 2 ? gemv_act_launch<BITS, XT, 2, 1>(p, st) : gemv_act_launch<BITS, XT, 8, 1>(p, st);
+    else
+        return false;
+    return true;
+}
+
 template <typename XT>
 cudaError_t gemv_run_x(gq::GemvArgs p, cudaStream_t st) {
     TimedScope ts__("dequant_gemv", st);
@@ -560,6 +770,13 @@ cudaError_t gemv_run_x(gq::GemvArgs p, cudaStream_t st) {
             case 4: return gemv_mma_run<4, XT>(p, st);
             default: return gemv_mma_run<8, XT>(p, st);
         }
+    }
+    cudaError_t e;
+    switch (p.bits) {
+        case 2: if (gemv_act_run<2, XT>(p, st, &e)) return e; break;
+        case 3: if (gemv_act_run<3, XT>(p, st, &e)) return e; break;
+        case 4: if (gemv_act_run<4, XT>(p, st, &e)) return e; break;
+        default: if (gemv_act_run<8, XT>(p, st, &e)) return e; break;
     }
     p.nblocks = (unsigned)((p.N + 31) / 32);
     const long long blocks = (long long)p.nblocks * ((p.M + gq::GV_TOK - 1) / gq::GV_TOK);
