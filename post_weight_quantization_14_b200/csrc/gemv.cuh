@@ -282,11 +282,12 @@ struct GmCfg {
     static constexpr int SMEM = STAGES * STAGE > SUMS ? STAGES * STAGE : SUMS;
 };
 
-template <int BITS, typename XT, int MT, bool G16>
+// GROUPS: those of 128 columns, at most: 1 (groups of 128, or one per row), 4 (64 and 32) or 8 (16).
+template <int BITS, typename XT, int MT, int GROUPS>
 __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs p) {
     using Cfg = GmCfg<BITS, XT, MT>;
     constexpr int TOK = Cfg::TOK, STAGES = Cfg::STAGES;
-    constexpr int GROUPS = G16 ? 8 : 4;   // of 128 columns, at most
+    constexpr bool G16 = GROUPS == 8;
     extern __shared__ __align__(128) uint8_t gm_smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
     const int nw = warp & 3, kg = warp >> 2;
@@ -301,23 +302,25 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
     // ---- copies into the ring: BITS x 16 bytes of words and MT x 8 elements of X a thread and stage
     const int wrows = (int)(((long long)K * BITS + 31) / 32);
     const int lc = tid & 31, lr = tid >> 5;   // this thread's 16-byte column (8-element chunk of X) and first row
-    const int32_t* wsrc = p.qweight + ((long long)st0 * Cfg::WROWS + lr) * p.N + nc + 4 * lc;
-    const long long left = p.N - (nc + 4 * lc), step8 = 8 * p.N;   // rows n from this column on; words of 8 rows
-    const int wleft = left > 0 ? wrows - lr : 0;
+    // Where N is no multiple of 4, a row of words starts up to 3 words past a 16-byte boundary: the copy
+    // starts at the boundary, brings one piece more, and the reader skips the 'skew' words.
+    const int nmod = (int)p.N & 3, skew = lr * nmod & 3;
+    const int32_t* wsrc = p.qweight + ((long long)st0 * Cfg::WROWS + lr) * p.N + nc + 4 * lc - skew;
+    const long long left = p.N - (nc + 4 * lc) + skew, step8 = 8 * p.N;   // words of the row from here on; of 8 rows
+    const uint32_t full = left > 0 ? 16 : 0, tail = left >= 4 ? 16 : left > 0 ? 4 * (uint32_t)left : 0;
     auto issue = [&](int st) {
         const uint32_t base = smem_u32(gm_smem) + (uint32_t)((st - st0) % STAGES) * Cfg::STAGE;
         const uint32_t dst = base + (uint32_t)(lr * GM_WSTRIDE + 16 * lc);
-        const int rows = wleft - st * Cfg::WROWS;   // this thread's words in the stage: 8 i < rows
+        const int rows = wrows - lr - st * Cfg::WROWS;   // rows from this thread's first on
 #pragma unroll
         for (int i = 0; i < BITS; ++i) {
-            if (p.vec) {
-                cp_async_zfill<16>(dst + 8 * i * GM_WSTRIDE, 8 * i < rows ? wsrc : p.qweight, 8 * i < rows ? 16 : 0);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const bool in = 8 * i < rows && left > c;
-                    cp_async_zfill<4>(dst + 8 * i * GM_WSTRIDE + 4 * c, in ? wsrc + c : p.qweight, in ? 4 : 0);
-                }
+            // the row after the array's last word must not be touched: the last row ends where it ends
+            const uint32_t bytes = 8 * i + 1 < rows ? full : 8 * i + 1 == rows ? tail : 0;
+            cp_async_zfill<16>(dst + 8 * i * GM_WSTRIDE, bytes ? wsrc : p.qweight, bytes);
+            if (nmod && lc == 31) {
+                const long long more = left - 4;
+                const uint32_t extra = more <= 0 || 8 * i + 1 > rows ? 0 : 8 * i + 1 < rows || more >= 4 ? 16 : 4 * (uint32_t)more;
+                cp_async_zfill<16>(dst + 8 * i * GM_WSTRIDE + 16, extra ? wsrc + 4 : p.qweight, extra);
             }
             wsrc += step8;
         }
@@ -362,7 +365,8 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
             const int kk = k + (G16 ? 16 : 32) * i;
-            if (kk < K && (G16 || (kk & gmask) == 0 || (i == 0 && start))) load_group(kk >> p.gshift, s_next[i], z_next[i]);
+            if (kk < K && (G16 || (GROUPS == 1 && p.gshift == 7) || (kk & gmask) == 0 || (i == 0 && start)))
+                load_group(kk >> p.gshift, s_next[i], z_next[i]);
         }
     };
 
@@ -418,14 +422,21 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
         const uint8_t* base = gm_smem + (st - st0) % STAGES * Cfg::STAGE;
         const uint8_t* wbase = base + kg * (Cfg::W_BYTES / 2) + (32 * nw + 4 * gid) * 4;
         const uint8_t* xbase = base + Cfg::W_BYTES + gid * Cfg::XSTRIDE + 128 * kg * (int)sizeof(XT);
-        auto row = [&](int r) { return *reinterpret_cast<const uint4*>(wbase + r * GM_WSTRIDE); };
+        auto row = [&](int r) {
+            const uint8_t* w = wbase + r * GM_WSTRIDE;
+            if (!nmod) return *reinterpret_cast<const uint4*>(w);
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(w) + (r * nmod & 3);
+            return make_uint4(u[0], u[1], u[2], u[3]);
+        };
         const int k0 = st * GM_K + 128 * kg;
 #pragma unroll
         for (int s4 = 0; s4 < 4; ++s4) {
             const int k = k0 + 32 * s4;
             if (k >= K) break;
-            if constexpr (!G16) {
-                if ((k & gmask) == 0 || (s4 == 0 && st == st0)) use_group(s_raw[s4], z_raw[s4]);
+            if constexpr (GROUPS == 1) {
+                if (s4 == 0 && (p.gshift == 7 || st == st0)) use_group(s_raw[0], z_raw[0]);
+            } else if constexpr (GROUPS == 4) {
+                if ((k & gmask) == 0) use_group(s_raw[s4], z_raw[s4]);
             }
             uint32_t xb[MT][4];
 #pragma unroll
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
                         mma_16816(part[j][mt], a[2], b[2], a[3], b[3], xb[mt][2], xb[mt][3], XT());
                     }
                 }
-                if (p.gshift <= 7 && (((k + 32) & gmask) == 0 || k + 32 >= K)) flush();
+                if (GROUPS == 1 ? p.gshift == 7 && (s4 == 3 || k + 32 >= K) : ((k + 32) & gmask) == 0 || k + 32 >= K) flush();
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -675,10 +686,10 @@ namespace gqh {
 
 int num_sms();
 
-template <int BITS, typename XT, int MT, bool G16>
+template <int BITS, typename XT, int MT, int GROUPS>
 cudaError_t gemv_mma_launch(gq::GemvArgs p, cudaStream_t st) {
     using Cfg = gq::GmCfg<BITS, XT, MT>;
-    constexpr auto kern = gq::gemv_mma_kernel<BITS, XT, MT, G16>;
+    constexpr auto kern = gq::gemv_mma_kernel<BITS, XT, MT, GROUPS>;
     GQ_TRY((smem_attr_once<kern, Cfg::SMEM>()));
     p.nblocks = (unsigned)((p.N + gq::GM_ROWS - 1) / gq::GM_ROWS);
     p.vec = p.N % 4 == 0;
@@ -714,10 +725,13 @@ cudaError_t gemv_mma_launch(gq::GemvArgs p, cudaStream_t st) {
 
 template <int BITS, typename XT>
 cudaError_t gemv_mma_run(const gq::GemvArgs& p, cudaStream_t st) {
-    if (p.g == 16 && !p.g_all) return gemv_mma_launch<BITS, XT, 2, true>(p, st);
-    if (p.M <= 8) return gemv_mma_launch<BITS, XT, 1, false>(p, st);
-    if (p.M <= 16) return gemv_mma_launch<BITS, XT, 2, false>(p, st);
-    return gemv_mma_launch<BITS, XT, 4, false>(p, st);
+    if (p.g_all || p.g == 128) {
+        if (p.M <= 8) return gemv_mma_launch<BITS, XT, 1, 1>(p, st);
+        if (p.M <= 16) return gemv_mma_launch<BITS, XT, 2, 1>(p, st);
+        return gemv_mma_launch<BITS, XT, 4, 1>(p, st);
+    }
+    if (p.g == 16) return gemv_mma_launch<BITS, XT, 2, 8>(p, st);
+    return p.M <= 8 ? gemv_mma_launch<BITS, XT, 1, 4>(p, st) : gemv_mma_launch<BITS, XT, 4, 4>(p, st);
 }
 
 template <int BITS, typename XT, int TM, int NL>
