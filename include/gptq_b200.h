@@ -272,8 +272,8 @@ gptq_status gptq_dequant_gemm(const void* X, int64_t M, const int32_t* qweight, 
  *   Y        device [M, d_out] row-major, bf16 or fp32 (yt), written in full; apart from the inputs.
  * Sums are fp32 in a fixed order (the same bits on every run); no rounded copy of W_hat is made,
  * and a bf16 Y is rounded once.  A non-finite X makes its own row of Y non-finite and no other.
- * Requires 1 <= M <= GPTQ_GEMV_MAX_M, d_in % 8 == 0, 1 <= d_out; X aligned to 8 elements,
- * qweight, scales and qzeros to 16 bytes.  No workspace, nothing is allocated. */
+ * Requires 1 <= M <= GPTQ_GEMV_MAX_M, d_in % 8 == 0, 1 <= d_out; X, qweight, scales and qzeros
+ * 16-byte aligned.  No workspace, nothing is allocated. */
 #define GPTQ_GEMV_MAX_M 64
 gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale, int64_t M, const int32_t* qweight,
                               const uint16_t* scales, const int32_t* qzeros, const int32_t* g_idx, int64_t d_out,

@@ -16,9 +16,9 @@
 // thread's word of 8 codes (row n, columns k .. k + 7) is four pairs (i, i + 4) that mask out of the
 // word side by side, and its 16 bytes of X (token, k .. k + 7) are the matching pairs.  q - z is exact
 // in bf16 and fp16, P = X (q - z)^T is summed over a group and enters y as s P in fp32.
-// A CTA owns 128 rows n and a run of columns.  Words and X arrive in a ring of stages of 256 columns
-// by asynchronous copies, which keeps some 100 KB in flight on an SM without registers; four warps
-// take 32 rows each of a stage's first 128 columns, four of the others.  The halves' sums, and those of
+// A CTA owns 128 rows n and a run of columns.  One warp fills a ring of stages of 256 columns with
+// TMA (or bulk
+// copies of rows), which keeps some 100 KB in flight on an SM and costs the others no issue slots; four warps take 32 rows each of a stage's first 128 columns, four of the others.  The halves' sums, and those of
 // the CTAs of a cluster that split K, are joined in a fixed order through shared memory.
 //
 // gemv_act_kernel (g_idx: any column in any group; see there), and gemv_lane_kernel for layers with so
@@ -28,6 +28,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "dqgemm_e4m3.cuh"
 #include "pack.cuh"
 
 namespace gq {
@@ -53,6 +54,7 @@ struct GemvArgs {
     unsigned nblocks;         // blocks of rows n
     unsigned split;           // CTAs of a cluster, which split K
     int vec;                  // N % 4 == 0: 16-byte loads of packed words
+    int tma;                  // words and X by TMA
     int gshift;               // log2 g, or 31 for one group per row
 };
 
@@ -121,6 +123,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// (a & mask) | c as one instruction: with both constants as immediates the compiler takes two.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(c));
+    return r;
 }
 template <typename T>
 __device__ __forceinline__ uint32_t bits_of(const T& v) {
@@ -200,14 +208,14 @@ __device__ __forceinline__ void w_pairs(uint32_t w, uint32_t w2, uint32_t zz, ui
     if constexpr (BITS <= 4) {   // 0x4300 | q is the bf16 of 128 + q
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            v[i] = bits_of(__hsub2(as_bf162(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u), as_bf162(zz)));
+            v[i] = bits_of(__hsub2(as_bf162(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), as_bf162(zz)));
     } else {                     // both nibbles this way, then 16 high + (low - z): 8 significant bits
         const __nv_bfloat162 c128 = as_bf162(0x43004300u), c16 = as_bf162(0x41804180u);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const uint32_t two = __byte_perm(w, w2, i | ((i + 4) << 8));   // bytes i in the two halves
-            const __nv_bfloat162 lo = __hsub2(as_bf162((two & 0x000F000Fu) | 0x43004300u), c128);
-            const __nv_bfloat162 hi = __hsub2(as_bf162(((two >> 4) & 0x000F000Fu) | 0x43004300u), c128);
+            const __nv_bfloat162 lo = __hsub2(as_bf162(and_or(two, 0x000F000Fu, 0x43004300u)), c128);
+            const __nv_bfloat162 hi = __hsub2(as_bf162(and_or(two >> 4, 0x000F000Fu, 0x43004300u)), c128);
             v[i] = bits_of(__hfma2(hi, c16, __hsub2(lo, as_bf162(zz))));
         }
     }
@@ -221,14 +229,14 @@ __device__ __forceinline__ void w_pairs(uint32_t w, uint32_t w2, uint32_t zz, ui
 #pragma unroll
         for (int i = 0; i < NP; i += 2) {
             const uint32_t x = w >> (4 * i);
-            v[i] = bits_of(__hsub2(as_half2((x & 0x000F000Fu) | 0x64006400u), za));
-            v[i + 1] = bits_of(__hfma2(as_half2((x & 0x00F000F0u) | 0x64006400u), c16, zb));
+            v[i] = bits_of(__hsub2(as_half2(and_or(x, 0x000F000Fu, 0x64006400u)), za));
+            v[i + 1] = bits_of(__hfma2(as_half2(and_or(x, 0x00F000F0u, 0x64006400u)), c16, zb));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const uint32_t two = __byte_perm(w, w2, i | ((i + 4) << 8));
-            v[i] = bits_of(__hsub2(as_half2((two & 0x00FF00FFu) | 0x64006400u), as_half2(zz)));
+            v[i] = bits_of(__hsub2(as_half2(and_or(two, 0x00FF00FFu, 0x64006400u)), as_half2(zz)));
         }
     }
 }
@@ -263,34 +271,39 @@ __device__ __forceinline__ uint32_t zero_pair(uint32_t z, __nv_fp8_e4m3) {
     return z * 0x00010001u | 0x64006400u;   // 1024 + z, twice
 }
 
-constexpr int GM_THREADS = 256;    // eight warps: four of 32 rows n each, times two runs of columns
+constexpr int GM_WARPS = 8;        // four of 32 rows n each, times two runs of columns
+constexpr int GM_THREADS = 32 * GM_WARPS + 32;   // and one that fills the ring
 constexpr int GM_ROWS = 128;       // rows n of a CTA
 constexpr int GM_K = 256;          // columns of a stage, 128 for each half of the warps
-constexpr int GM_WSTRIDE = 4 * GM_ROWS + 32;   // bytes of a row of words: 16-byte reads without bank conflicts
+constexpr int GM_WSTRIDE = 4 * GM_ROWS + 32;   // bytes of a row of words: 16-byte reads without bank conflicts, room to skew
 
-template <int BITS, typename XT, int MT>
+template <int BITS, typename XT, int MT, int GROUPS>
 struct GmCfg {
+    static constexpr int CTAS = MT == 4 || GROUPS == 8 ? 1 : 2;   // to an SM, as registers go
     static constexpr int TOK = 8 * MT;
     static constexpr int WROWS = GM_K * BITS / 32;
+    static constexpr int W_BOX = WROWS * 128;   // 32 rows n by TMA
     static constexpr int W_BYTES = WROWS * GM_WSTRIDE;
     // the reads of eight (16-byte) or sixteen (8-byte) lanes fall into different banks
     static constexpr int XSTRIDE = GM_K * (int)sizeof(XT) + (sizeof(XT) == 2 ? 64 : 32);
-    static constexpr int STAGE = W_BYTES + TOK * XSTRIDE;
-    static constexpr int FIT = 110 * 1024 / STAGE;   // two CTAs to an SM
-    static constexpr int STAGES = FIT > 4 ? 4 : FIT < 2 ? 2 : FIT;
+    static constexpr int STAGE = (W_BYTES + TOK * XSTRIDE + 1023) / 1024 * 1024;   // TMA's swizzle
+    static constexpr int FIT = 220 / CTAS * 1024 / STAGE;
+    static constexpr int STAGES = FIT > 8 / CTAS ? 8 / CTAS : FIT < 2 ? 2 : FIT;
     static constexpr int SUMS = 2 * TOK * GM_ROWS * 4;
-    static constexpr int SMEM = STAGES * STAGE > SUMS ? STAGES * STAGE : SUMS;
+    static constexpr int SMEM = 1024 + (STAGES * STAGE > SUMS ? STAGES * STAGE : SUMS);
+    static_assert(W_BYTES % 128 == 0, "TMA's destination");
 };
 
 // GROUPS: those of 128 columns, at most: 1 (groups of 128, or one per row), 4 (64 and 32) or 8 (16).
 template <int BITS, typename XT, int MT, int GROUPS>
-__global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs p) {
-    using Cfg = GmCfg<BITS, XT, MT>;
+__global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS) gemv_mma_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const GemvArgs p) {
+    using Cfg = GmCfg<BITS, XT, MT, GROUPS>;
     constexpr int TOK = Cfg::TOK, STAGES = Cfg::STAGES;
     constexpr bool G16 = GROUPS == 8;
-    extern __shared__ __align__(128) uint8_t gm_smem[];
+    extern __shared__ uint8_t gm_raw[];
+    uint8_t* gm_smem = gm_raw + (-smem_u32(gm_raw) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
-    const int nw = warp & 3, kg = warp >> 2;
+    const int nw = warp & 3, kg = warp >> 2 & 1;
     const unsigned cta = blockIdx.x / p.split, rank = blockIdx.x % p.split;
     const long long nc = (long long)(cta % p.nblocks) * GM_ROWS;   // the CTA's first row
     const int m0 = (int)(cta / p.nblocks) * TOK;
@@ -299,40 +312,93 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
     const int nst = (K + GM_K - 1) / GM_K;
     const int st0 = (int)((long long)nst * rank / p.split), st1 = (int)((long long)nst * (rank + 1) / p.split);
 
-    // ---- copies into the ring: BITS x 16 bytes of words and MT x 8 elements of X a thread and stage
-    const int wrows = (int)(((long long)K * BITS + 31) / 32);
-    const int lc = tid & 31, lr = tid >> 5;   // this thread's 16-byte column (8-element chunk of X) and first row
-    // Where N is no multiple of 4, a row of words starts up to 3 words past a 16-byte boundary: the copy
-    // starts at the boundary, brings one piece more, and the reader skips the 'skew' words.
-    const int nmod = (int)p.N & 3, skew = lr * nmod & 3;
-    const int32_t* wsrc = p.qweight + ((long long)st0 * Cfg::WROWS + lr) * p.N + nc + 4 * lc - skew;
-    const long long left = p.N - (nc + 4 * lc) + skew, step8 = 8 * p.N;   // words of the row from here on; of 8 rows
-    const uint32_t full = left > 0 ? 16 : 0, tail = left >= 4 ? 16 : left > 0 ? 4 * (uint32_t)left : 0;
-    auto issue = [&](int st) {
-        const uint32_t base = smem_u32(gm_smem) + (uint32_t)((st - st0) % STAGES) * Cfg::STAGE;
-        const uint32_t dst = base + (uint32_t)(lr * GM_WSTRIDE + 16 * lc);
-        const int rows = wrows - lr - st * Cfg::WROWS;   // rows from this thread's first on
+    __shared__ uint64_t full[STAGES], empty[STAGES];   // a lane of the copying warp each; a warp of the others each
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&full[i], p.tma ? 1 : 32);
+            mbar_init(&empty[i], GM_WARPS);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+
+    // Without TMA (N no multiple of 4, or e4m3 rows that are no multiple of 16 bytes) rows that start
+    // between two 16-byte boundaries are copied from the boundary on, and the reader skips the 'skew'.
+    const int nmod = (int)p.N & 3;
+    if (warp == GM_WARPS) {
+        // ---- copies into the ring
+        if (p.tma && lane == 0) {
+            prefetch_tmap(&mW);
+            prefetch_tmap(&mX);
+        }
+        const long long wtotal = ((long long)K * BITS + 31) / 32 * p.N, xtotal = (long long)p.M * K;
+        const int wrows = (int)(((long long)K * BITS + 31) / 32), cols = (int)min((long long)GM_ROWS, p.N - nc);
+        bool ok = true;
+        int st = st0;
+        for (; st < st1 && ok; ++st) {
+            const int slot = (st - st0) % STAGES;
+            ok = __all_sync(~0u, mbar_wait(&empty[slot], (((st - st0) / STAGES) & 1) ^ 1, st));
+            if (!ok) break;
+            uint8_t* base = gm_smem + slot * Cfg::STAGE;
+            if (p.tma) {   // four boxes of 32 rows n and one of X; what lies outside the arrays comes as zeros
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[slot], Cfg::W_BOX * 4 + TOK * GM_K * (int)sizeof(XT));
 #pragma unroll
-        for (int i = 0; i < BITS; ++i) {
-            // the row after the array's last word must not be touched: the last row ends where it ends
-            const uint32_t bytes = 8 * i + 1 < rows ? full : 8 * i + 1 == rows ? tail : 0;
-            cp_async_zfill<16>(dst + 8 * i * GM_WSTRIDE, bytes ? wsrc : p.qweight, bytes);
-            if (nmod && lc == 31) {
-                const long long more = left - 4;
-                const uint32_t extra = more <= 0 || 8 * i + 1 > rows ? 0 : 8 * i + 1 < rows || more >= 4 ? 16 : 4 * (uint32_t)more;
-                cp_async_zfill<16>(dst + 8 * i * GM_WSTRIDE + 16, extra ? wsrc + 4 : p.qweight, extra);
+                    for (int i = 0; i < 4; ++i)
+                        tma_load_2d(base + i * Cfg::W_BOX, &mW, &full[slot], (int)nc + 32 * i, st * Cfg::WROWS);
+                    tma_load_2d(base + Cfg::W_BYTES, &mX, &full[slot], st * GM_K, m0);
+                }
+                continue;
             }
-            wsrc += step8;
-        }
-        const int k = st * GM_K + 8 * lc;
+            // Otherwise a lane copies whole rows in pieces of 16 bytes, as far as the array goes, and the up
+            // to three words behind the last piece singly.
+            constexpr int WR = (Cfg::WROWS + 31) / 32, XE = 16 / (int)sizeof(XT), XR = (TOK + 31) / 32;
+            long long wat[WR], xat[XR];
+            int wn[WR], xn[XR];
+            uint32_t bytes = 0;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int r = lr + 8 * i;
-            const bool in = m0 + r < p.M && k < K;
-            cp_async_zfill<8 * sizeof(XT)>(base + Cfg::W_BYTES + (uint32_t)(r * Cfg::XSTRIDE + lc * 8 * (int)sizeof(XT)),
-                                           in ? X + (long long)(m0 + r) * K + k : X, in ? 8 * sizeof(XT) : 0);
+            for (int i = 0; i < WR; ++i) {
+                const int r = lane + 32 * i, row = st * Cfg::WROWS + r;
+                wn[i] = 0;
+                if (r < Cfg::WROWS && row < wrows) {
+                    const int skew = r * nmod & 3, need = cols + skew;
+                    wat[i] = (long long)row * p.N + nc - skew;
+                    wn[i] = (int)min((long long)((need + 3) & ~3), (wtotal - wat[i]) & ~3ll);
+                    for (int j = wn[i]; j < need; ++j)
+                        reinterpret_cast<int32_t*>(base + r * GM_WSTRIDE)[j] = p.qweight[wat[i] + j];
+                    bytes += 4 * wn[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < XR; ++i) {
+                const int r = lane + 32 * i;
+                xn[i] = 0;
+                if (r < TOK && m0 + r < p.M) {
+                    xat[i] = (long long)(m0 + r) * K + st * GM_K;
+                    const int skew = (int)(xat[i] % XE), need = min(GM_K, K - st * GM_K) + skew;
+                    xat[i] -= skew;
+                    xn[i] = (int)min((long long)((need + XE - 1) & ~(XE - 1)), (xtotal - xat[i]) & ~(long long)(XE - 1));
+                    if (xn[i] < need)   // eight elements of e4m3
+                        *reinterpret_cast<uint2*>(base + Cfg::W_BYTES + r * Cfg::XSTRIDE + xn[i] * (int)sizeof(XT)) =
+                            *reinterpret_cast<const uint2*>(X + xat[i] + xn[i]);
+                    bytes += xn[i] * (int)sizeof(XT);
+                }
+            }
+            mbar_arrive_expect_tx(&full[slot], bytes);
+#pragma unroll
+            for (int i = 0; i < WR; ++i)
+                if (wn[i] > 0) bulk_g2s(base + (lane + 32 * i) * GM_WSTRIDE, p.qweight + wat[i], 4 * wn[i], &full[slot]);
+#pragma unroll
+            for (int i = 0; i < XR; ++i)
+                if (xn[i] > 0)
+                    bulk_g2s(base + Cfg::W_BYTES + (lane + 32 * i) * Cfg::XSTRIDE, X + xat[i], xn[i] * (int)sizeof(XT),
+                             &full[slot]);
         }
-    };
+        // after a wait that ran out, the copies still in flight land before the CTA leaves
+        for (int i = max(st0, st - STAGES); !ok && i < st; ++i)
+            (void)mbar_wait(&full[(i - st0) % STAGES], ((i - st0) / STAGES) & 1, -1);
+    }
 
     // ---- scales and zero points of this thread's rows n0 .. n0 + 3, one stage ahead, as loaded
     const long long n0 = nc + 32 * nw + 4 * gid;
@@ -399,33 +465,28 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
                 }
     };
 
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
-        if (st0 + i < st1) issue(st0 + i);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    if (st0 < st1) load_groups(st0 * GM_K + 128 * kg, true);
-    for (int st = st0; st < st1; ++st) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-        __syncthreads();   // the stage is complete, and everybody has left the one that is refilled
-        if (st + STAGES - 1 < st1) issue(st + STAGES - 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-
+    const int last = warp < GM_WARPS ? st1 : st0;   // the copying warp has no share in the sums
+    if (st0 < last) load_groups(st0 * GM_K + 128 * kg, true);
+    for (int st = st0; st < last; ++st) {
+        const int slot = (st - st0) % STAGES;
+        if (!__all_sync(~0u, mbar_wait(&full[slot], ((st - st0) / STAGES) & 1, st))) break;
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
             s_raw[i] = s_next[i];
 #pragma unroll
             for (int j = 0; j < ZW; ++j) z_raw[i][j] = z_next[i][j];
         }
-        if (st + 1 < st1) load_groups(st * GM_K + 128 * kg + GM_K, false);
+        if (st + 1 < last) load_groups(st * GM_K + 128 * kg + GM_K, false);
 
-        const uint8_t* base = gm_smem + (st - st0) % STAGES * Cfg::STAGE;
-        const uint8_t* wbase = base + kg * (Cfg::W_BYTES / 2) + (32 * nw + 4 * gid) * 4;
-        const uint8_t* xbase = base + Cfg::W_BYTES + gid * Cfg::XSTRIDE + 128 * kg * (int)sizeof(XT);
+        const uint8_t* base = gm_smem + slot * Cfg::STAGE;
+        const uint8_t* wbase = p.tma ? base + nw * Cfg::W_BOX + kg * (Cfg::W_BOX / 2)
+                                     : base + kg * (Cfg::WROWS / 2 * GM_WSTRIDE) + (32 * nw + 4 * gid) * 4;
+        const int xstride = p.tma ? GM_K * (int)sizeof(XT) : Cfg::XSTRIDE;
+        const uint8_t* xbase = base + Cfg::W_BYTES + gid * xstride + 128 * kg * (int)sizeof(XT);
+        // four neighbouring rows n of a row of words; TMA's boxes have 128-byte rows, 16-byte pieces swizzled
         auto row = [&](int r) {
-            const uint8_t* w = wbase + r * GM_WSTRIDE;
-            if (!nmod) return *reinterpret_cast<const uint4*>(w);
-            const uint32_t* u = reinterpret_cast<const uint32_t*>(w) + (r * nmod & 3);
+            if (p.tma) return *reinterpret_cast<const uint4*>(wbase + r * 128 + ((gid ^ (r + Cfg::WROWS / 2 * kg & 7)) << 4));
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(wbase + r * GM_WSTRIDE) + (r * nmod & 3);
             return make_uint4(u[0], u[1], u[2], u[3]);
         };
         const int k0 = st * GM_K + 128 * kg;
@@ -441,11 +502,19 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
             uint32_t xb[MT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const XT* x = reinterpret_cast<const XT*>(xbase + 8 * mt * Cfg::XSTRIDE) + 32 * s4;
+                const XT* x = reinterpret_cast<const XT*>(xbase + 8 * mt * xstride) + 32 * s4 +
+                              (sizeof(XT) == 1 && !p.tma ? (m0 + gid + 8 * mt) * K & 8 : 0);
                 if constexpr (G16)
                     x_pairs<true>(load_x44(x + 4 * tig, x + 16 + 4 * tig), xb[mt]);
                 else
                     x_pairs<false>(load_x8(x + 8 * tig), xb[mt]);
+                if (k + 32 > K) {   // past the last column the ring holds what was there before
+                    const bool lo = k + (G16 ? 4 : 8) * tig < K, hi = G16 ? k + 16 + 4 * tig < K : lo;
+                    xb[mt][0] = lo ? xb[mt][0] : 0u;
+                    xb[mt][1] = lo ? xb[mt][1] : 0u;
+                    xb[mt][2] = hi ? xb[mt][2] : 0u;
+                    xb[mt][3] = hi ? xb[mt][3] : 0u;
+                }
             }
             if constexpr (!G16) {
                 uint4 w = row(s4 * BITS + (BITS == 8 ? 2 * tig : BITS == 4 ? tig : BITS == 2 ? tig >> 1 : 3 * tig >> 2));
@@ -491,20 +560,24 @@ __global__ void __launch_bounds__(GM_THREADS, 2) gemv_mma_kernel(const GemvArgs 
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
     }
     if (p.gshift > 7) flush();   // one group per row
 
     // ---- join the two runs of columns, then the CTAs of the cluster, in a fixed order
-    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     float* sums = reinterpret_cast<float*>(gm_smem);   // [2][TOK][GM_ROWS]
+    if (warp < GM_WARPS) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                sums[(kg * TOK + 8 * mt + 2 * tig + (c & 1)) * GM_ROWS + 32 * nw + 4 * gid + j + (c & 2)] = total[j][mt][c];
+                for (int c = 0; c < 4; ++c)
+                    sums[(kg * TOK + 8 * mt + 2 * tig + (c & 1)) * GM_ROWS + 32 * nw + 4 * gid + j + (c & 2)] =
+                        total[j][mt][c];
+    }
     __syncthreads();
     auto finish = [&](int e, float y) {
         const int m = m0 + e / GM_ROWS;
@@ -688,16 +761,16 @@ int num_sms();
 
 template <int BITS, typename XT, int MT, int GROUPS>
 cudaError_t gemv_mma_launch(gq::GemvArgs p, cudaStream_t st) {
-    using Cfg = gq::GmCfg<BITS, XT, MT>;
+    using Cfg = gq::GmCfg<BITS, XT, MT, GROUPS>;
     constexpr auto kern = gq::gemv_mma_kernel<BITS, XT, MT, GROUPS>;
     GQ_TRY((smem_attr_once<kern, Cfg::SMEM>()));
     p.nblocks = (unsigned)((p.N + gq::GM_ROWS - 1) / gq::GM_ROWS);
     p.vec = p.N % 4 == 0;
     p.gshift = p.g_all ? 31 : p.g == 128 ? 7 : p.g == 64 ? 6 : p.g == 32 ? 5 : 4;
     const long long blocks = (long long)p.nblocks * ((p.M + Cfg::TOK - 1) / Cfg::TOK);
-    // K is split over a cluster where that shortens the run: waves of two CTAs to an SM, times the
+    // K is split over a cluster where that shortens the run: waves of CTAs, times the
     // stages of a CTA and about one for its start and end.
-    const long long nst = (p.K + gq::GM_K - 1) / gq::GM_K, slots = 2ll * num_sms();
+    const long long nst = (p.K + gq::GM_K - 1) / gq::GM_K, slots = (long long)Cfg::CTAS * num_sms();
     long long best = 0;
     for (unsigned s = 1; s <= 8 && s <= nst; s *= 2) {
         const long long cost = (blocks * s + slots - 1) / slots * ((nst + s - 1) / s + 1);
@@ -718,7 +791,14 @@ cudaError_t gemv_mma_launch(gq::GemvArgs p, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    CUtensorMap mw = {}, mx = {};
+    p.tma = p.vec && (sizeof(XT) == 2 || p.K % 16 == 0);
+    if (p.tma && (!tmap_2d(&mw, p.qweight, CU_TENSOR_MAP_DATA_TYPE_INT32, 4, (uint64_t)((p.K * BITS + 31) / 32),
+                           (uint64_t)p.N, Cfg::WROWS, 32, true) ||
+                  !tmap_2d(&mx, p.X, sizeof(XT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                           (int)sizeof(XT), (uint64_t)p.M, (uint64_t)p.K, Cfg::TOK, gq::GM_K, false)))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
     if (e != cudaSuccess) (void)cudaGetLastError();
     return e;
 }

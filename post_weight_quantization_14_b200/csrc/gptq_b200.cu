@@ -659,9 +659,8 @@ gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale
         return fail(GPTQ_ERR_INVALID_ARG, "M must be in [1, %d] (got %lld)", GPTQ_GEMV_MAX_M, (long long)M);
     if ((cfg->desc_act != 0) != (g_idx != nullptr))
         return fail(GPTQ_ERR_INVALID_ARG, "g_idx must be given iff desc_act is not 0");
-    if (misaligned(X, xt == GPTQ_BF16 ? 16 : 8) || misaligned(x_scale, 4) || misaligned(g_idx, 4) ||
-        misaligned(Y, yt == GPTQ_BF16 ? 2 : 4))
-        return fail(GPTQ_ERR_INVALID_ARG, "X must be aligned to 8 elements, x_scale, g_idx and Y to their own");
+    if (!aligned16(X) || misaligned(x_scale, 4) || misaligned(g_idx, 4) || misaligned(Y, yt == GPTQ_BF16 ? 2 : 4))
+        return fail(GPTQ_ERR_INVALID_ARG, "X must be 16-byte aligned, x_scale, g_idx and Y to their elements");
     gq::GemvArgs p{};
     p.X = X;
     p.x_scale = x_scale;
