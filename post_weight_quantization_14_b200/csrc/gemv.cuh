@@ -279,7 +279,7 @@ constexpr int GM_WSTRIDE = 4 * GM_ROWS + 32;   // bytes of a row of words: 16-by
 
 template <int BITS, typename XT, int MT, int GROUPS>
 struct GmCfg {
-    static constexpr int CTAS = MT == 4 || GROUPS == 8 ? 1 : 2;   // to an SM, as registers go
+    static constexpr int CTAS = MT == 4 || GROUPS == 8 ? 1 : MT == 1 && GROUPS == 1 && BITS <= 4 ? 3 : 2;   // to an SM, as registers go
     static constexpr int TOK = 8 * MT;
     static constexpr int WROWS = GM_K * BITS / 32;
     static constexpr int W_BOX = WROWS * 128;   // 32 rows n by TMA
@@ -288,7 +288,7 @@ struct GmCfg {
     static constexpr int XSTRIDE = GM_K * (int)sizeof(XT) + (sizeof(XT) == 2 ? 64 : 32);
     static constexpr int STAGE = (W_BYTES + TOK * XSTRIDE + 1023) / 1024 * 1024;   // TMA's swizzle
     static constexpr int FIT = 220 / CTAS * 1024 / STAGE;
-    static constexpr int STAGES = FIT > 8 / CTAS ? 8 / CTAS : FIT < 2 ? 2 : FIT;
+    static constexpr int STAGES = FIT > 4 ? 4 : FIT < 2 ? 2 : FIT;
     static constexpr int SUMS = 2 * TOK * GM_ROWS * 4;
     static constexpr int SMEM = 1024 + (STAGES * STAGE > SUMS ? STAGES * STAGE : SUMS);
     static_assert(W_BYTES % 128 == 0, "TMA's destination");
@@ -811,7 +811,9 @@ cudaError_t gemv_mma_run(const gq::GemvArgs& p, cudaStream_t st) {
         return gemv_mma_launch<BITS, XT, 4, 1>(p, st);
     }
     if (p.g == 16) return gemv_mma_launch<BITS, XT, 2, 8>(p, st);
-    return p.M <= 8 ? gemv_mma_launch<BITS, XT, 1, 4>(p, st) : gemv_mma_launch<BITS, XT, 4, 4>(p, st);
+    if (p.M <= 8) return gemv_mma_launch<BITS, XT, 1, 4>(p, st);
+    if (p.M <= 16) return gemv_mma_launch<BITS, XT, 2, 4>(p, st);
+    return gemv_mma_launch<BITS, XT, 4, 4>(p, st);
 }
 
 template <int BITS, typename XT, int TM, int NL>
