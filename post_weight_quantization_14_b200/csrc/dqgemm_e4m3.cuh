@@ -52,7 +52,7 @@ constexpr int D8_EPI_WARP0 = 8, D8_PROD_WARP = 16;   // converters 0-7, epilogue
 constexpr int D8_AST = 3, D8_PST = 4, D8_LAG = 2;
 // Registers a thread after setmaxnreg, per warpgroup.  A split above what the launch gave would wait
 // forever, so the launch checks that the kernel was compiled to D8_REGS.
-constexpr int D8_REGS = 96, D8_REGS_CONV = 72, D8_REGS_EPI = 136, D8_REGS_MISC = 64;
+constexpr int D8_REGS = 96, D8_REGS_CONV = 56, D8_REGS_EPI = 160, D8_REGS_MISC = 48;
 static_assert(2 * D8_REGS_CONV + 2 * D8_REGS_EPI + D8_REGS_MISC <= D8_THREADS / 128 * D8_REGS, "register split");
 constexpr int D8_PAR_S = 1024, D8_PAR_Z = 256;   // bytes of scales and zero points of four groups
 constexpr int D8_SEG_TILES = 4;   // K tiles per segment for one group per row: 16 MMAs in place
@@ -99,6 +99,18 @@ __device__ __forceinline__ void umma_e4m3_ta(uint32_t d, uint32_t a, uint64_t bd
         "r"(a), "l"(bdesc), "r"(idesc), "r"(acc));
 }
 
+// Whether a barrier's phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -144,28 +156,14 @@ __device__ __forceinline__ void codes_to_bytes(const uint32_t (&w)[BITS], uint32
     }
 }
 
-// Pairs of fp32 in one 64-bit register: acc += s * v for both halves.
-using pair_t = unsigned long long;
-__device__ __forceinline__ pair_t pair(uint32_t lo, uint32_t hi) {
-    pair_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-    return v;
-}
-__device__ __forceinline__ void fma2(pair_t& acc, pair_t s, pair_t v) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(s), "l"(v));
-}
-__device__ __forceinline__ float pair_get(pair_t v, int hi) {
-    return __uint_as_float((uint32_t)(hi ? v >> 32 : v));
-}
-
 // One lane's column of C rows of Y, scaled; rows past the end are left alone.
 __device__ __forceinline__ void put(float* y, float v) { *y = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
 template <int C, typename YT>
-__device__ __forceinline__ void store_rows(YT* y, int ld, int rows, const pair_t (&acc)[C / 2], const float* xs) {
+__device__ __forceinline__ void store_rows(YT* y, int ld, int rows, const float (&acc)[C], const float* xs) {
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-        if (j < rows) put(y, pair_get(acc[j / 2], j & 1) * xs[j]);
+        if (j < rows) put(y, acc[j] * xs[j]);
         y += ld;
     }
 }
@@ -317,50 +315,56 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
             asm volatile("bar.sync 1, 256;" ::: "memory");   // the previous tile's scales are read
             if (et < TT) xs[et] = m0 + et < p.M ? p.x_scale[m0 + et] : 0.f;
             asm volatile("bar.sync 1, 256;" ::: "memory");
-            pair_t acc[C / 2];
+            float acc[C];
 #pragma unroll
-            for (int j = 0; j < C / 2; ++j) acc[j] = 0;
-            // the scale of group g
+            for (int j = 0; j < C; ++j) acc[j] = 0.f;
+            // the scales of four groups, the next one in the low half of .x
             const int groups = p.spt ? nseg : 1;
-            auto scale = [&](int g) {
-                if ((g & 3) == 0) ok = warp_wait(w, &pfull[unit % D8_PST], (unit / D8_PST) & 1);
-                const __half h = reinterpret_cast<const __half*>(
-                    par + (unit % D8_PST) * (D8_PAR_S + D8_PAR_Z))[128 * (g & 3) + 32 * qd + lane];
-                if ((g & 3) == 3 || g == groups - 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&pempty[unit % D8_PST]);
-                    __syncwarp();
-                    ++unit;
-                }
-                return h;
+            uint2 sq = {0, 0};
+            auto scales = [&] {
+                ok = warp_wait(w, &pfull[unit % D8_PST], (unit / D8_PST) & 1);
+                const uint16_t* sp = reinterpret_cast<const uint16_t*>(par + (unit % D8_PST) * (D8_PAR_S + D8_PAR_Z)) +
+                                     32 * qd + lane;
+                sq.x = sp[0] | (uint32_t)sp[128] << 16;
+                sq.y = sp[256] | (uint32_t)sp[384] << 16;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pempty[unit % D8_PST]);
+                __syncwarp();
+                ++unit;
             };
-            __half s_next = __float2half(0.f);
-            if (ok) s_next = scale(0);
+            scales();
+            bool ready = false;   // the next accumulator was complete when last looked at
             for (int sg = 0; sg < nseg && ok; ++sg) {
-                const uint32_t sf = __float_as_uint(512.f * __half2float(s_next));   // P_g comes as 2^-9 P_g
-                const pair_t s = pair(sf, sf);
-                ok = warp_wait(w, &dfull[buf], dph);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < C / 32; ++c) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(tmem + buf * TT + col0 + 32 * c + lane_off, r);
-                    if (c == 0 && sg + 1 < groups) s_next = scale(sg + 1);
-                    tmem_ld_wait();
-                    if (c == C / 32 - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&dempty[buf]);
-                        __syncwarp();
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, pair(r[2 * j], r[2 * j + 1]));
+                const float s = 512.f * __half2float(__ushort_as_half((uint16_t)sq.x));   // P_g comes as 2^-9 P_g
+                if (!ready) {
+                    ok = warp_wait(w, &dfull[buf], dph);
+                    if (!ok) break;
                 }
+                tc_fence_after();
+                uint32_t r[C / 32][32];
+#pragma unroll
+                for (int c = 0; c < C / 32; ++c) tmem_ld_32x32b_x32(tmem + buf * TT + col0 + 32 * c + lane_off, r[c]);
+                if (sg + 1 < groups) {
+                    if ((sg & 3) == 3) {
+                        scales();
+                    } else {
+                        sq.x = sq.x >> 16 | sq.y << 16;
+                        sq.y >>= 16;
+                    }
+                }
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&dempty[buf]);
+                __syncwarp();
                 if (++buf == nd) {
                     buf = 0;
                     dph ^= 1;
                 }
+                // looked at here, the barrier's latency passes under the multiplications
+                ready = __all_sync(~0u, mbar_test_wait(&dfull[buf], dph));
+#pragma unroll
+                for (int j = 0; j < C; ++j) acc[j] = fmaf(s, __uint_as_float(r[j / 32][j % 32]), acc[j]);
             }
             const int j0 = half * C;   // this warp's first token of the tile
             if (p.split == 1) {
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                 if (ok) {
 #pragma unroll
                     for (int j = 0; j < C; ++j)
-                        red[(j0 + j) * 128 + 32 * qd + lane] = pair_get(acc[j / 2], j & 1);
+                        red[(j0 + j) * 128 + 32 * qd + lane] = acc[j];
                 }
                 __syncwarp();
                 cluster_sync_all();
