@@ -49,7 +49,7 @@ namespace gq {
 
 constexpr int D8_THREADS = 640;
 constexpr int D8_EPI_WARP0 = 8, D8_PROD_WARP = 16;   // converters 0-7, epilogue 8-15, TMA 16, MMA 17, scales 18
-constexpr int D8_AST = 3, D8_PST = 4, D8_LAG = 2;
+constexpr int D8_AST = 3, D8_PST = 8, D8_LAG = 2;
 // Registers a thread after setmaxnreg, per warpgroup.  A split above what the launch gave would wait
 // forever, so the launch checks that the kernel was compiled to D8_REGS.
 constexpr int D8_REGS = 96, D8_REGS_CONV = 56, D8_REGS_EPI = 160, D8_REGS_MISC = 48;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
     uint64_t* dfull = aempty + D8_AST;                       // [ND] segment complete
     uint64_t* dempty = dfull + ND;                        // [ND] segment drained
     uint64_t* pfull = dempty + ND;                        // [PST] scales and zero points landed
-    uint64_t* pempty = pfull + D8_PST;                       // [PST] read by converters and epilogue
+    uint64_t* pempty = pfull + D8_PST;                       // [PST] scales read by the epilogue's warps, zero points used
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pempty + D8_PST);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
         }
         for (int s = 0; s < D8_PST; ++s) {
             mbar_init(&pfull[s], 1);
-            mbar_init(&pempty[s], 16);
+            mbar_init(&pempty[s], 9);
         }
         fence_mbar_init();
     }
@@ -251,31 +251,38 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
         const int qd = warp & 3, t = 32 * qd + lane;
         const uint32_t set = warp >> 2;
         const uint32_t a_row = a_ring + ((uint32_t)(32 * qd) << 16);
-        uint32_t it = 0, unit = 0;
+        // units of four groups in a tile, and where the zero points of an operand's columns go stale:
+        // with every K tile, with every tile (one group per row) or never (no zero points given)
+        const uint32_t units = p.spt ? (nseg + 3) / 4 : 1;
+        uint32_t it0 = 0, unit0 = 0, seen = ~0u;   // of the tile; last unit waited for
         bool ok = true;
-        for (int w = first; w < p.tiles && ok; w += step) {
-            for (int kt = 0; kt < nkt; ++kt, ++it) {
-                // groups of this K tile, counted from the CTA's first: four to a unit
-                const int grp = kt * p.spt;
-                const uint8_t* zq = par + (unit % D8_PST) * (D8_PAR_S + D8_PAR_Z) + D8_PAR_S;
-                if ((it & 1) == set) {
-                    const uint32_t s = it % STAGES, a = it % D8_AST;
-                    ok = warp_wait(w, &full[s], (it / STAGES) & 1, true, &aempty[a], ((it / D8_AST) & 1) ^ 1, true,
-                                   &pfull[unit % D8_PST], (unit / D8_PST) & 1, true);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t* col =
-                        reinterpret_cast<const uint32_t*>(smem + s * Cfg::STAGE_BYTES + Cfg::X_BYTES) + t;
-                    const uint32_t dst = a_row + a_cols * a;
+        for (int w = first; w < p.tiles && ok; w += step, it0 += nkt, unit0 += units) {
+            for (int kt = (int)((it0 ^ set) & 1); kt < nkt; kt += 2) {
+                const uint32_t it = it0 + kt, s = it % STAGES, a = it % D8_AST;
+                const int grp = kt * p.spt;   // the K tile's first group, counted from the CTA's first
+                const bool write_z = p.qzeros == nullptr ? it < D8_AST : p.spt || kt < D8_AST;
+                const uint32_t unit = unit0 + (uint32_t)grp / 4;
+                const bool fresh = p.qzeros != nullptr && unit != seen;
+                ok = warp_wait(w, &full[s], (it / STAGES) & 1, true, &aempty[a], ((it / D8_AST) & 1) ^ 1, true,
+                               &pfull[unit % D8_PST], (unit / D8_PST) & 1, fresh);
+                if (!ok) break;
+                seen = unit;
+                tc_fence_after();
+                const uint32_t* col =
+                    reinterpret_cast<const uint32_t*>(smem + s * Cfg::STAGE_BYTES + Cfg::X_BYTES) + t;
+                const uint32_t dst = a_row + a_cols * a;
+                uint32_t words[4][BITS];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t words[2][BITS], r[16];
+                for (int i = 0; i < 4 * BITS; ++i) words[i / BITS][i % BITS] = col[i * 128];
 #pragma unroll
-                        for (int i = 0; i < 2 * BITS; ++i) words[i / BITS][i % BITS] = col[(2 * BITS * h + i) * 128];
-                        codes_to_bytes<BITS>(words[0], r);
-                        codes_to_bytes<BITS>(words[1], r + 8);
-                        tmem_st_32x32b_x16(dst + 16 * h, r);
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[16];
+                    codes_to_bytes<BITS>(words[2 * h], r);
+                    codes_to_bytes<BITS>(words[2 * h + 1], r + 8);
+                    tmem_st_32x32b_x16(dst + 16 * h, r);
+                }
+                if (write_z) {
+                    const uint8_t* zq = par + (unit % D8_PST) * (D8_PAR_S + D8_PAR_Z) + D8_PAR_S;
                     for (int q = 0; q < (p.spt ? p.spt : 1); ++q) {   // each group's zero point, -z 2^-9
                         uint32_t z = 1u << (BITS - 1);
                         if (p.qzeros != nullptr) {
@@ -289,16 +296,12 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                         const uint32_t r[8] = {z, z, z, z, z, z, z, z};
                         tmem_st_32x32b_x8(dst + 32 + 8 * q, r);
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&conv[a]);
                 }
-                if (kt == nkt - 1 || ((grp + p.spt) & 3) == 0 && p.spt) {   // the unit is used up
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&pempty[unit % D8_PST]);
-                    ++unit;
-                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&conv[a]);
+                __syncwarp();
             }
         }
     } else if (warp < D8_PROD_WARP) {
@@ -319,7 +322,6 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < C; ++j) acc[j] = 0.f;
             // the scales of four groups, the next one in the low half of .x
-            const int groups = p.spt ? nseg : 1;
             uint2 sq = {0, 0};
             auto scales = [&] {
                 ok = warp_wait(w, &pfull[unit % D8_PST], (unit / D8_PST) & 1);
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                 __syncwarp();
                 ++unit;
             };
-            scales();
+            if (ok) scales();
             bool ready = false;   // the next accumulator was complete when last looked at
             for (int sg = 0; sg < nseg && ok; ++sg) {
                 const float s = 512.f * __half2float(__ushort_as_half((uint16_t)sq.x));   // P_g comes as 2^-9 P_g
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                 uint32_t r[C / 32][32];
 #pragma unroll
                 for (int c = 0; c < C / 32; ++c) tmem_ld_32x32b_x32(tmem + buf * TT + col0 + 32 * c + lane_off, r[c]);
-                if (sg + 1 < groups) {
+                if (p.spt && sg + 1 < nseg) {
                     if ((sg & 3) == 3) {
                         scales();
                     } else {
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
         // ---------------- MMA issuer: the whole warp waits, one elected lane issues
         constexpr uint32_t idesc = make_idesc(0u, 128, TT);   // e4m3 x e4m3 -> fp32
         const bool lead = elect_one();
-        uint32_t it = 0, buf = 0, dph = 1;
+        uint32_t it = 0, buf = 0, dph = 1, unit = 0;
         bool ok = true;
         // One K tile: MM = MMAs (32 columns each) per segment.  A segment of every group opens
         // and closes within the tile; with one group per row it spans D8_SEG_TILES tiles.
@@ -524,6 +526,11 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                     const int segs = min(p.spt, nseg - kt * p.spt);
                     ok = p.spt == 2 ? issue(std::integral_constant<int, 2>{}, s, a, segs, true, true, w)
                                     : issue(std::integral_constant<int, 1>{}, s, a, segs, true, true, w);
+                }
+                // the products of a unit's last K tile come after its zero points were read
+                if (kt == nkt - 1 || (p.spt && ((kt + 1) * p.spt & 3) == 0)) {
+                    if (lead && ok) umma_commit(&pempty[unit % D8_PST]);
+                    ++unit;
                 }
             }
         }
