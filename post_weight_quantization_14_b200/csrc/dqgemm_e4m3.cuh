@@ -68,7 +68,7 @@ struct D8Cfg {
     static constexpr int C = TT / 2;                  // tokens per epilogue warp
     static constexpr int ND = 384 / TT;               // accumulators, at most (see acc_cols)
     static constexpr int SMEM =
-        1024 + STAGES * STAGE_BYTES + D8_PST * (D8_PAR_S + D8_PAR_Z) + 4 * TT + 512;
+        1024 + STAGES * STAGE_BYTES + D8_PST * (D8_PAR_S + D8_PAR_Z) + 8 * TT + 512;
     static_assert(STAGE_BYTES % 1024 == 0, "the swizzled tiles stay 1024-byte aligned");
     static_assert(TT * 128 * 4 <= STAGES * STAGE_BYTES, "partial sums fit the ring");
 };
@@ -162,9 +162,14 @@ __device__ __forceinline__ void put(__nv_bfloat16* y, float v) { *y = __float2bf
 template <int C, typename YT>
 __device__ __forceinline__ void store_rows(YT* y, int ld, int rows, const float (&acc)[C], const float* xs) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-        if (j < rows) put(y, acc[j] * xs[j]);
-        y += ld;
+    for (int j = 0; j < C; j += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(xs + j);
+        const float xv[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (j + i < rows) put(y, acc[j + i] * xv[i]);
+            y += ld;
+        }
     }
 }
 
@@ -190,8 +195,8 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset, so that accesses stay shared-memory ones
     uint8_t* par = smem + STAGES * Cfg::STAGE_BYTES;   // [PST] scales [4][128] fp16, zero points [4][16] words
-    float* xs = reinterpret_cast<float*>(par + D8_PST * (D8_PAR_S + D8_PAR_Z));   // [TT] scales of the tile's tokens
-    uint64_t* full = reinterpret_cast<uint64_t*>(xs + TT);   // [STAGES] TMA landed
+    float* xs = reinterpret_cast<float*>(par + D8_PST * (D8_PAR_S + D8_PAR_Z));   // [2][TT] scales of the tokens of this tile and the next
+    uint64_t* full = reinterpret_cast<uint64_t*>(xs + 2 * TT);   // [STAGES] TMA landed
     uint64_t* empty = full + STAGES;                         // [STAGES] MMAs of the stage done
     uint64_t* conv = empty + STAGES;                         // [AST] A operand written
     uint64_t* aempty = conv + D8_AST;                        // [AST] A operand read
@@ -313,11 +318,18 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
         const int et = threadIdx.x - 32 * D8_EPI_WARP0;
         uint32_t buf = 0, dph = 0, unit = 0;   // accumulator and its phase
         bool ok = true;   // once false, the loop goes on without waiting: its barriers need every warp
-        for (int w = first; w < p.tiles; w += step) {
+        // The tokens' scales are fetched a tile ahead, as their way from memory is longer than a K tile.
+        auto token_scale = [&](int w) {
+            const int m = (w / p.tiles_n) * TT + et;
+            return et < TT && w < p.tiles && m < p.M ? p.x_scale[m] : 0.f;
+        };
+        int xs_off = 0;
+        float xs_next = token_scale(first);
+        for (int w = first; w < p.tiles; w += step, xs_off ^= TT) {
             const int n = (w % p.tiles_n) * 128 + 32 * qd + lane, m0 = (w / p.tiles_n) * TT;
-            asm volatile("bar.sync 1, 256;" ::: "memory");   // the previous tile's scales are read
-            if (et < TT) xs[et] = m0 + et < p.M ? p.x_scale[m0 + et] : 0.f;
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            // the other half is free: every warp has passed the barrier below since it was read
+            if (et < TT) xs[xs_off + et] = xs_next;
+            xs_next = token_scale(w + step);
             float acc[C];
 #pragma unroll
             for (int j = 0; j < C; ++j) acc[j] = 0.f;
@@ -369,14 +381,15 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                 for (int j = 0; j < C; ++j) acc[j] = fmaf(s, __uint_as_float(r[j / 32][j % 32]), acc[j]);
             }
             const int j0 = half * C;   // this warp's first token of the tile
+            asm volatile("bar.sync 1, 256;" ::: "memory");   // the tokens' scales are written
             if (p.split == 1) {
                 if (ok && n < p.N) {
                     const int rows = p.M - m0 - j0;
                     const long long at = (long long)(m0 + j0) * p.N + n;
                     if (p.y_bf16)
-                        store_rows<C>(reinterpret_cast<__nv_bfloat16*>(p.Y) + at, p.N, rows, acc, xs + j0);
+                        store_rows<C>(reinterpret_cast<__nv_bfloat16*>(p.Y) + at, p.N, rows, acc, xs + xs_off + j0);
                     else
-                        store_rows<C>(reinterpret_cast<float*>(p.Y) + at, p.N, rows, acc, xs + j0);
+                        store_rows<C>(reinterpret_cast<float*>(p.Y) + at, p.N, rows, acc, xs + xs_off + j0);
                 }
             } else {
                 // One tile per cluster.  The partial sums take the ring's place once the last MMAs
@@ -397,7 +410,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                         float y = 0.f;
                         for (int r = 0; r < p.split; ++r)
                             y += ld_cluster_f32(smem_u32(red + j * 128 + c), (uint32_t)r);
-                        store_y(p.Y, p.y_bf16, (long long)(m0 + j) * p.N + nn, y * xs[j]);
+                        store_y(p.Y, p.y_bf16, (long long)(m0 + j) * p.N + nn, y * xs[xs_off + j]);
                     }
                 }
                 __syncwarp();
