@@ -2,20 +2,20 @@
 //
 //   Y[m, n] = xs[m] sum_g s_g[n] P_g[n, m],   P_g[n, m] = sum_{k in g} (q[n, k] - z_g[n]) X8[m, k]
 //
-// q - z of 2, 3 and 4 bits lies in [-15, 15] and is exact in e4m3, so P_g is formed by the 8-bit
-// tensor instructions (twice the bf16 rate) from exact products with fp32 accumulation; s_g and
-// xs are applied in fp32.  No rounded copy of W_hat is made.
+// Codes and zero points of 2, 3 and 4 bits are exact in e4m3, so P_g is formed by the 8-bit tensor
+// instructions (twice the bf16 rate) from exact products with fp32 accumulation; s_g and xs are
+// applied in fp32.  No rounded copy of W_hat is made.
 //
 // The weights are the A operand (128 rows n of a tile) and sit in tensor memory: a converter
-// thread owns one row, turns its packed codes into e4m3 bytes and stores them with one
-// tcgen05.st, so shared memory carries only X8 (the B operand) and the packed words.  With rows
-// on the lanes, a group's scale is one register of an epilogue thread.
+// thread owns one row, turns its packed codes into e4m3 bytes and stores them with tcgen05.st, so
+// shared memory carries only X8 (the B operand) and the packed words.  With rows on the lanes, a
+// group's scale is one register of an epilogue thread.
 //
-// A tile is 128 rows x TT tokens, K advances by 128.  One CTA per SM, 20 warps:
-//   warps 0-7    converters, two sets that take turns, a thread per row, a ring of four A
-//                operands of 32 columns;
+// A tile is 128 rows x TT tokens (64 up to 64 tokens, else 128), K advances by 128.  One CTA per SM,
+// 20 warps:
+//   warps 0-7    converters, two sets that take turns, a thread per row, a ring of three A operands;
 //   warps 8-15   epilogue: two warps per lane quadrant, TT / 2 tokens each, running sums in
-//                registers: y += s_g P_g, two at a time;
+//                registers: y += s_g P_g;
 //   warp 16      TMA: X8 tile (TT tokens x 128 bytes, 128-byte swizzle) and packed words
 //                (4 BITS words x 128 rows) into a ring of stages;
 //   warp 17      MMA issuer: per quantization group one accumulator segment, in a ring of
@@ -29,9 +29,18 @@
 // arithmetic sequence), so spreading the codes to bytes already gives q 2^-9, and 0x80 | z is -z 2^-9.
 // P_g 2^-9 = sum q 2^-9 X8 + sum (-z 2^-9) X8: the second sum takes the same MMAs again with an
 // operand of 32 equal columns.  That doubles the tensor work, which had three quarters of the time to
-// spare, and more than halves the converters' integer work, which bound the kernel: looking q - z up
-// in registers by byte permutes took 11 instructions for 8 codes against 5 (4096 x 4096 x 2048
-// tokens: 83 us against 78 us).
+// spare, and more than halves the converters' integer work: looking q - z up in registers by byte
+// permutes took 11 instructions for 8 codes against 5 (4096 x 4096 x 2048 tokens: 83 us against 78 us
+// when this was chosen).
+//
+// What bounds it: each 128-column K tile takes about 900 clocks, of which the MMAs are 520 (eight of
+// 65 clocks) and an epilogue warp and a converter set are busy for most of it.  Neither leaving out the
+// code conversion (-3 %), the multiplications by s_g (-6 %) nor the second MMA pass (-9 %) changes it
+// much, nor a third converter set, nor a ring of six A operands with two accumulators: the roles'
+// latencies (a passed barrier is 100-200 clocks) are close to each other.  4-bit groups of 128:
+// 2048 tokens x 4096 x 4096 in 72 us (950 TFLOP/s), 8192 tokens x 11008 x 4096 in 647 us
+// (1140 TFLOP/s, 35 % of the 8-bit rate); groups of 32 take 174 us for the former, as every group is an
+// accumulator to drain.
 //
 // Few tiles: the K range is split over a cluster of S CTAs, whose partial sums are joined
 // through distributed shared memory in rank order.
@@ -633,6 +642,7 @@ cudaError_t dq_gemm_e4m3_launch(const uint8_t* X8, const int32_t* qweight, gq::D
     return e;
 }
 
+// Up to 64 tokens a tile of 64: 64 x 4096 x 4096 took 11.9 us against 15.8 us padded to 128.
 template <int BITS>
 cudaError_t dq_gemm_e4m3_run(const uint8_t* X8, const int32_t* qweight, const gq::D8Args& p, cudaStream_t st) {
     if (p.M <= 64) return dq_gemm_e4m3_launch<BITS, 64>(X8, qweight, p, st);

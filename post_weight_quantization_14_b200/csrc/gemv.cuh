@@ -16,13 +16,22 @@
 // thread's word of 8 codes (row n, columns k .. k + 7) is four pairs (i, i + 4) that mask out of the
 // word side by side, and its 16 bytes of X (token, k .. k + 7) are the matching pairs.  q - z is exact
 // in bf16 and fp16, P = X (q - z)^T is summed over a group and enters y as s P in fp32.
-// A CTA owns 128 rows n and a run of columns.  One warp fills a ring of stages of 256 columns with
-// TMA (or bulk
-// copies of rows), which keeps some 100 KB in flight on an SM and costs the others no issue slots; four warps take 32 rows each of a stage's first 128 columns, four of the others.  The halves' sums, and those of
-// the CTAs of a cluster that split K, are joined in a fixed order through shared memory.
+// A CTA owns 128 rows n and a run of columns.  One warp fills a ring of stages of 256 columns with TMA
+// (or bulk copies of rows), which keeps some 100 KB in flight on an SM and costs the others no issue
+// slots; four warps take 32 rows each of a stage's first 128 columns, four of the others.  The halves'
+// sums, and those of the CTAs of a cluster that split K, are joined in a fixed order through shared
+// memory.
+//
+// Measured, packed words from memory: 4-bit groups of 128, one token through 4096 x 4096 7.5 us (8.9 MB,
+// 1.2 TB/s: of that about 3 us are launch, first loads and the join), through 11008 x 4096 14.5 us; eight
+// e4m3 tokens through 50001 x 8192 (odd row count: bulk copies of rows) 101 us (214 MB, 2.1 TB/s); 16
+// tokens through 11008 x 4096, 3 bits, groups of 64, 34 us.  The copies alone would take a third of
+// that: the time is instruction issue and the fixed cost of a stage (a barrier to pass, scales, a flush
+// per group).
 //
 // gemv_act_kernel (g_idx: any column in any group; see there), and gemv_lane_kernel for layers with so
-// many groups that its table does not fit: one lane per row n, eight warps split the columns.
+// many groups that its table does not fit (above 1280): one lane per row n, eight warps split the columns,
+// latency-bound and meant for correctness alone.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -279,7 +288,9 @@ constexpr int GM_WSTRIDE = 4 * GM_ROWS + 32;   // bytes of a row of words: 16-by
 
 template <int BITS, typename XT, int MT, int GROUPS>
 struct GmCfg {
-    static constexpr int CTAS = MT == 4 || GROUPS == 8 ? 1 : MT == 1 && GROUPS == 1 && BITS <= 4 ? 3 : 2;   // to an SM, as registers go
+    // CTAs of an SM, as registers go: 3 against 2 for up to eight tokens took the 50001 x 8192 product
+    // above from 123 to 101 us
+    static constexpr int CTAS = MT == 4 || GROUPS == 8 ? 1 : MT == 1 && GROUPS == 1 && BITS <= 4 ? 3 : 2;
     static constexpr int TOK = 8 * MT;
     static constexpr int WROWS = GM_K * BITS / 32;
     static constexpr int W_BOX = WROWS * 128;   // 32 rows n by TMA
@@ -296,7 +307,8 @@ struct GmCfg {
 
 // GROUPS: those of 128 columns, at most: 1 (groups of 128, or one per row), 4 (64 and 32) or 8 (16).
 template <int BITS, typename XT, int MT, int GROUPS>
-__global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS) gemv_mma_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const GemvArgs p) {
+__global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
+    gemv_mma_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const GemvArgs p) {
     using Cfg = GmCfg<BITS, XT, MT, GROUPS>;
     constexpr int TOK = Cfg::TOK, STAGES = Cfg::STAGES;
     constexpr bool G16 = GROUPS == 8;
@@ -485,7 +497,8 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
         const uint8_t* xbase = base + Cfg::W_BYTES + gid * xstride + 128 * kg * (int)sizeof(XT);
         // four neighbouring rows n of a row of words; TMA's boxes have 128-byte rows, 16-byte pieces swizzled
         auto row = [&](int r) {
-            if (p.tma) return *reinterpret_cast<const uint4*>(wbase + r * 128 + ((gid ^ (r + Cfg::WROWS / 2 * kg & 7)) << 4));
+            if (p.tma)
+                return *reinterpret_cast<const uint4*>(wbase + r * 128 + ((gid ^ (r + Cfg::WROWS / 2 * kg & 7)) << 4));
             const uint32_t* u = reinterpret_cast<const uint32_t*>(wbase + r * GM_WSTRIDE) + (r * nmod & 3);
             return make_uint4(u[0], u[1], u[2], u[3]);
         };
@@ -534,7 +547,9 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
                         mma_16816(part[j][mt], a[2], b[2], a[3], b[3], xb[mt][2], xb[mt][3], XT());
                     }
                 }
-                if (GROUPS == 1 ? p.gshift == 7 && (s4 == 3 || k + 32 >= K) : ((k + 32) & gmask) == 0 || k + 32 >= K) flush();
+                if (GROUPS == 1 ? p.gshift == 7 && (s4 == 3 || k + 32 >= K)
+                                : ((k + 32) & gmask) == 0 || k + 32 >= K)
+                    flush();
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -606,7 +621,9 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
 // point) in fp16, and a lane's 4 (or, where there are too many groups for that, 1) rows are neighbours:
 // one read gives a column's entries for them, and the packed words are read along n.  A warp takes
 // chunks of 8 columns; the 8 warps of a CTA and the CTAs of a cluster split K.  s (q - z) (at most
-// 11 + 8 significant bits) is exact in fp32, and sums are fp32.
+// 11 + 8 significant bits) is exact in fp32, and sums are fp32.  Bound by instruction issue, about ten a
+// weight for two tokens (two tokens through 4096 x 11008: 39 us, eight: 119 us); lookups in global memory
+// instead, by gemv_lane_kernel, took 436 us for two.
 constexpr int GA_THREADS = 256;
 constexpr int GA_TABLE = 160 * 1024;   // bytes of the table, at most
 
@@ -803,6 +820,8 @@ cudaError_t gemv_mma_launch(gq::GemvArgs p, cudaStream_t st) {
     return e;
 }
 
+// The token tile follows M, as every tile of 8 tokens costs its MMAs whether it is filled or not (16
+// tokens in a tile of 16 against one of 32: 34 us against 42 us, 3 bits, groups of 64, 11008 x 4096).
 template <int BITS, typename XT>
 cudaError_t gemv_mma_run(const gq::GemvArgs& p, cudaStream_t st) {
     if (p.g_all || p.g == 128) {
@@ -844,7 +863,8 @@ cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
     return e;
 }
 
-// True where the table of gemv_act_kernel fits; the launch's status is then in *e.
+// True where the table of gemv_act_kernel fits; the launch's status is then in *e.  Two tokens at a time
+// up to M = 2, for fewer registers and more CTAs on an SM.
 template <int BITS, typename XT>
 bool gemv_act_run(const gq::GemvArgs& p, cudaStream_t st, cudaError_t* e) {
     if ((long long)p.ng * 128 * 4 <= gq::GA_TABLE)

@@ -8,6 +8,10 @@
 // r is positive and common to a row, so it scales a but cancels from the codes: one sum and one
 // maximum per row suffice, and they are taken together.  |v| is compared by its bit pattern,
 // whose order is that of the magnitudes with NaN above infinity, so a NaN reaches x_scale.
+//
+// Bound by memory for many rows: 2048 x 4096 bf16 with residual 12 us (58.7 MB, 4.7 TB/s; of it about
+// 2 us launch and tail), 8192 rows 37 us (6.3 TB/s), 4096 x 11008 bf16 without norm 27 us (5.0 TB/s),
+// 8191 x 16384 fp32 135 us (5.0 TB/s); by latency for few: 2.0 us for one row to 64.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

@@ -194,6 +194,25 @@ def test_gemm_e4m3_matches_fp64(M, d_out, d_in, bits, g, sym, y):
     assert torch.equal(first, Y)
 
 
+# More tiles than SMs: blocks go from tile to tile, with odd and even counts of K tiles, groups that end
+# inside one, and zero points that change with the group, with the tile or never.
+GEMM_MANY = [
+    (2100, 1288, 96, 3, -1, False, "f32"),
+    (2100, 1288, 160, 4, 32, False, "bf16"),
+    (2100, 1288, 384, 4, 128, False, "f32"),
+    (2100, 1288, 640, 4, -1, False, "f32"),
+    (2100, 1288, 896, 2, 64, True, "bf16"),
+    (2100, 1288, 2176, 4, 128, False, "f32"),
+    (2100, 1288, 1152, 4, -1, True, "f32"),
+    (40, 20488, 640, 4, 128, False, "f32"),
+]
+
+
+@pytest.mark.parametrize("M,d_out,d_in,bits,g,sym,y", GEMM_MANY)
+def test_gemm_e4m3_many_tiles(M, d_out, d_in, bits, g, sym, y):
+    test_gemm_e4m3_matches_fp64(M, d_out, d_in, bits, g, sym, y)
+
+
 @pytest.mark.parametrize("bits,act", [(4, 0), (3, 0), (8, 0), (4, 1)])
 def test_gemv_extreme_codes_scales_and_nonfinite_rows(bits, act):
     rng = np.random.default_rng(bits + act)
