@@ -282,6 +282,40 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
         : "memory");
     return v;
 }
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+// Sum, in rank order, of the PARTS floats (``stride`` bytes apart), or of four neighbours, at one
+// shared-memory address of the cluster's first ``split`` <= 8 CTAs.  The loads are all in flight
+// together: one by one, each costs its latency (some 250 clocks).
+template <int PARTS>
+__device__ __forceinline__ float cluster_sum(uint32_t addr, uint32_t stride, int split) {
+    float v[8][PARTS], y = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) v[r][i] = r < split ? ld_cluster_f32(addr + i * stride, (uint32_t)r) : 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) y += v[r][i];
+    return y;
+}
+__device__ __forceinline__ float4 cluster_sum4(uint32_t addr, int split) {
+    float4 v[8], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] = r < split ? ld_cluster_f32x4(addr, (uint32_t)r) : y;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) y = make_float4(y.x + v[r].x, y.y + v[r].y, y.z + v[r].z, y.w + v[r].w);
+    return y;
+}
 
 // tf32 split: x = hi + lo with hi = tf32(x) (round to nearest, ties away from zero) and
 // lo = tf32(x - hi).  The rounding works on the bit pattern: adding half a unit of the 13

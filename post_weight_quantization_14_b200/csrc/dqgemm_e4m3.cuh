@@ -412,14 +412,14 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                 }
                 __syncwarp();
                 cluster_sync_all();
-                // rank r finishes the tokens r, r + split, ...
-                const int c = et & 127, nn = (w % p.tiles_n) * 128 + c;
-                for (int j = rank + p.split * (et >> 7); j < TT; j += 2 * p.split) {
-                    if (m0 + j < p.M && nn < p.N) {
-                        float y = 0.f;
-                        for (int r = 0; r < p.split; ++r)
-                            y += ld_cluster_f32(smem_u32(red + j * 128 + c), (uint32_t)r);
-                        store_y(p.Y, p.y_bf16, (long long)(m0 + j) * p.N + nn, y * xs[xs_off + j]);
+                // rank r finishes the tokens r, r + split, ..., a warp a token; N is a multiple of 8
+                const int c = 4 * lane, nn = (w % p.tiles_n) * 128 + c;
+                for (int j = rank + p.split * ew; j < TT && m0 + j < p.M; j += 8 * p.split) {
+                    if (nn < p.N) {
+                        const float4 y = cluster_sum4(smem_u32(red + j * 128 + c), p.split);
+                        const float x = xs[xs_off + j];
+                        store_y4(p.Y, p.y_bf16, (long long)(m0 + j) * p.N + nn,
+                                 make_float4(y.x * x, y.y * x, y.z * x, y.w * x));
                     }
                 }
                 __syncwarp();

@@ -605,12 +605,8 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
     } else {
         __syncwarp();
         cluster_sync_all();
-        for (int e = (int)rank * GM_THREADS + tid; e < E; e += (int)p.split * GM_THREADS) {
-            float y = 0.f;
-            for (unsigned r = 0; r < p.split; ++r)
-                y += ld_cluster_f32(smem_u32(sums + e), r) + ld_cluster_f32(smem_u32(sums + E + e), r);
-            finish(e, y);
-        }
+        for (int e = (int)rank * GM_THREADS + tid; e < E; e += (int)p.split * GM_THREADS)
+            finish(e, cluster_sum<2>(smem_u32(sums + e), 4 * E, (int)p.split));
         __syncwarp();
         cluster_sync_all();   // no CTA leaves while its sums are being read
     }
@@ -760,11 +756,8 @@ __global__ void __launch_bounds__(GA_THREADS) gemv_act_kernel(const GemvArgs p) 
     if (p.split > 1) {
         __syncwarp();
         cluster_sync_all();
-        for (int e = (int)rank * GA_THREADS + tid; e < E; e += (int)p.split * GA_THREADS) {
-            float y = 0.f;
-            for (unsigned r = 0; r < p.split; ++r) y += ld_cluster_f32(smem_u32(sums + e), r);
-            finish(e, y);
-        }
+        for (int e = (int)rank * GA_THREADS + tid; e < E; e += (int)p.split * GA_THREADS)
+            finish(e, cluster_sum<1>(smem_u32(sums + e), 0, (int)p.split));
         __syncwarp();
         cluster_sync_all();   // no CTA leaves while its sums are being read
     }

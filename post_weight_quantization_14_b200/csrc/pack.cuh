@@ -72,6 +72,16 @@ __device__ __forceinline__ void store_y(void* Y, int bf16, long long at, float y
     else
         reinterpret_cast<float*>(Y)[at] = y;
 }
+// The same for four neighbours, of which the first lies on a multiple of four.
+__device__ __forceinline__ void store_y4(void* Y, int bf16, long long at, float4 y) {
+    if (bf16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(y.x, y.y), b = __floats2bfloat162_rn(y.z, y.w);
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(Y) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(Y) + at) = y;
+    }
+}
 
 // W_hat[o, c] = scale[g(c), o] * (q[o, c] - zero[g(c), o]); one thread per weight, row-major.
 // g(c) = c / g, or g_idx[c] when a per-column group index is given (activation ordering);
