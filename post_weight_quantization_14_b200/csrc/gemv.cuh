@@ -778,12 +778,14 @@ cudaError_t gemv_mma_launch(gq::GemvArgs p, cudaStream_t st) {
     p.vec = p.N % 4 == 0;
     p.gshift = p.g_all ? 31 : p.g == 128 ? 7 : p.g == 64 ? 6 : p.g == 32 ? 5 : 4;
     const long long blocks = (long long)p.nblocks * ((p.M + Cfg::TOK - 1) / Cfg::TOK);
-    // K is split over a cluster where that shortens the run: waves of CTAs, times the
-    // stages of a CTA and about one for its start and end.
-    const long long nst = (p.K + gq::GM_K - 1) / gq::GM_K, slots = (long long)Cfg::CTAS * num_sms();
+    // K is split over a cluster where that shortens the run.  An SM's time for its share of the CTAs, in
+    // tenths of a stage that a CTA does alone: k CTAs side by side take 3 + 7 k for a stage of each (1.7
+    // and 2.4 times a single one's, measured), and a wave takes 25 for its start and end.
+    const long long nst = (p.K + gq::GM_K - 1) / gq::GM_K;
     long long best = 0;
     for (unsigned s = 1; s <= 8 && s <= nst; s *= 2) {
-        const long long cost = (blocks * s + slots - 1) / slots * ((nst + s - 1) / s + 1);
+        const long long ctas = (blocks * s + num_sms() - 1) / num_sms(), waves = (ctas + Cfg::CTAS - 1) / Cfg::CTAS;
+        const long long cost = (nst + s - 1) / s * (3 * waves + 7 * ctas) + 25 * waves;
         if (s == 1 || cost < best) {
             best = cost;
             p.split = s;
