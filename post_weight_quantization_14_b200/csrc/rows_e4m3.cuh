@@ -10,8 +10,8 @@
 // whose order is that of the magnitudes with NaN above infinity, so a NaN reaches x_scale.
 //
 // Bound by memory for many rows: 2048 x 4096 bf16 with residual 12 us (58.7 MB, 4.7 TB/s; of it about
-// 2 us launch and tail), 8192 rows 37 us (6.3 TB/s), 4096 x 11008 bf16 without norm 27 us (5.0 TB/s),
-// 8191 x 16384 fp32 135 us (5.0 TB/s); by latency for few: 2.0 us for one row to 64.
+// 2 us launch and tail), 8192 rows 37 us (6.3 TB/s), 4096 x 11008 bf16 without norm 28 us (4.8 TB/s),
+// 8191 x 16384 fp32 138 us (4.9 TB/s, w re-read from L2 for every row); by latency for few: 2.0 us for one row to 64.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -77,15 +77,24 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
-// 448 v / a for eight values, rounded to nearest even.
-__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float f, float inv) {
+// What turns a row into codes: 448 v / a = (v f) (hi + lo), with 448 / (a f) = hi + lo to 48 bits.
+struct RowScale {
+    float f, hi, lo;
+};
+// 448 v / a for eight values, rounded to nearest even.  The quotient is rounded to fp32 once, from 48
+// bits: where it lies on the boundary between two codes, which happens often with bf16 rows, it is exact.
+__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], const RowScale& s) {
+    auto q = [&](int i) {
+        const float t = v[i] * s.f;
+        return fmaf(t, s.hi, t * s.lo);
+    };
     uint32_t r[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(v[4 * i] * f * inv, v[4 * i + 1] * f * inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(v[4 * i + 2] * f * inv, v[4 * i + 3] * f * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t lo =
+            __nv_cvt_float2_to_fp8x2(make_float2(q(4 * i), q(4 * i + 1)), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi =
+            __nv_cvt_float2_to_fp8x2(make_float2(q(4 * i + 2), q(4 * i + 3)), __NV_SATFINITE, __NV_E4M3);
         r[i] = lo | (hi << 16);
     }
     return make_uint2(r[0], r[1]);
@@ -118,9 +127,6 @@ __device__ __forceinline__ void rows_join(float& sum, uint32_t& top, bool warp_o
     }
 }
 
-struct RowScale {
-    float f, inv;   // X8 = e4m3((v f) inv)
-};
 template <bool NORM>
 __device__ __forceinline__ RowScale row_scale(const RowsArgs& p, float sum, uint32_t top, float* x_scale, bool first) {
     const float a = __uint_as_float(top);
@@ -131,7 +137,8 @@ __device__ __forceinline__ RowScale row_scale(const RowsArgs& p, float sum, uint
     // a below 2^-100 would overflow 448 / a: the row is lifted by 2^64 first, which is exact
     RowScale s;
     s.f = a < 0x1p-100f ? 0x1p64f : 1.f;
-    s.inv = a > 0.f ? 448.f / (a * s.f) : (a == 0.f ? 0.f : a);
+    s.hi = a > 0.f ? 448.f / (a * s.f) : (a == 0.f ? 0.f : a);
+    s.lo = a > 0.f && a <= 0x1p100f ? fmaf(-s.hi, a * s.f, 448.f) * (s.hi * (1.f / 448.f)) : 0.f;
     return s;
 }
 
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(rw_max_threads(VEC)) rows_e4m3_kernel(const Ro
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const int c = c0 + i * step;
-        if (c < D) *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(v[i], s.f, s.inv);
+        if (c < D) *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(v[i], s);
     }
 }
 
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(1024) rows_e4m3_long_kernel(const RowsArgs p) 
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[i] *= w[i];
         }
-        *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(h, s.f, s.inv);
+        *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(h, s);
     }
 }
 
@@ -266,7 +273,7 @@ cudaError_t rows_e4m3_run(gq::RowsArgs p, long long M, const char* name, cudaStr
     if (vecs > gq::RW_MAX_VECS)
         return launch_pdl(gq::rows_e4m3_long_kernel<XT, WT, NORM>, grid, dim3(1024), 0, st, p);
     // Few rows: a vector a thread, for latency.  Many rows: four, for bytes in flight and cheap barriers;
-    // eight for long rows without R, whose registers they leave enough of (4096 x 11008 bf16: 27 us against
+    // eight for long rows without R, whose registers they leave enough of (4096 x 11008 bf16: 28 us against
     // 32 us with four; with R they do not: 2048 x 11008 took 37 us against 29 us).
     const bool few = M <= 2 * num_sms();
     int vec = few ? 1 : p.R == nullptr && vecs > 512 ? 8 : 4, threads;

@@ -353,6 +353,20 @@ def test_quantize_e4m3_matches_fp64(M, d, xt):
     _check_rows(X8, xs, y, scale, d)
 
 
+@pytest.mark.parametrize("M,d", [(3, 64), (40, 1024), (500, 4096), (400, 8200), (5, 40000)])
+def test_quantize_e4m3_boundaries_between_codes(M, d):
+    # A bf16 v has 8 significant bits, and so has the row's maximum a; the boundary m between two codes
+    # has 5.  So 448 v - m a is a multiple of 2^-16 of its terms or 0: the fp64 quotient lies on the
+    # boundary exactly or far from it in units of fp32, and the codes are the same, ties to even.
+    rng = np.random.default_rng(M + d + 3)
+    X, Xv = _tensor(_activations(rng, M, d), "bf16")
+    X8, xs = torch.empty((M, d), dtype=torch.float8_e4m3fn, device=U_.dev()), torch.empty(M, device=U_.dev())
+    G.gptq_quantize_e4m3(X, X8, xs)
+    q = 448.0 * Xv / np.max(np.abs(Xv), axis=1, keepdims=True)
+    want = torch.from_numpy(q.astype(np.float32)).to(torch.float8_e4m3fn)
+    assert torch.equal(X8.cpu().float(), want.float())
+
+
 @pytest.mark.parametrize("d", [64, 8192, 65536])
 def test_rows_special_values(d):
     rng = np.random.default_rng(d)
