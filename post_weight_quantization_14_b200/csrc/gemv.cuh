@@ -613,32 +613,26 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
 }
 
 // Activation order: any column in any group.  The work is a lookup of a scale and a zero point for every
-// weight, so the CTA keeps those of all groups for its rows n in shared memory, as (scale, 1024 + zero
-// point) in fp16, and a lane's 4 (or, where there are too many groups for that, 1) rows are neighbours:
-// one read gives a column's entries for them, and the packed words are read along n.  A warp takes
-// chunks of 8 columns; the 8 warps of a CTA and the CTAs of a cluster split K.  s (q - z) (at most
-// 11 + 8 significant bits) is exact in fp32, and sums are fp32.  Bound by instruction issue, about ten a
-// weight for two tokens (two tokens through 4096 x 11008: 39 us, eight: 119 us); lookups in global memory
-// instead, by gemv_lane_kernel, took 436 us for two.
-constexpr int GA_THREADS = 256;
+// weight, so the CTA keeps those of all groups for its 32 rows n in shared memory, as (scale, 1024 + zero
+// point) in fp16: one 16-byte read gives a column's entries for the 4 neighbouring rows of a thread, and
+// the packed words are read along n.  A warp takes 32 columns at a time, in the fragment order of
+// gemv_mma_kernel; the 8 warps of a CTA and the CTAs of a cluster split K.  s (q - z) (at most 11 + 8
+// significant bits) is formed in fp32 without rounding and cut into bf16 parts that hold it exactly (two
+// for codes of up to 4 bits, three for 8 bits), so the products are exact and the sums fp32, and a
+// weight's decoding and cutting, some 14 instructions, serve up to 32 tokens.
+// Bound by instruction issue: 4096 x 11008, 4-bit groups of 128, 2 tokens 38 us, 16 tokens 42 us, 64
+// tokens in two tiles 105 us.  fp32 multiply-adds in place of the tensor instruction took 39 us for 2
+// tokens and 119 us for 8; lookups in global memory (gemv_lane_kernel) 436 us for 2.
+constexpr int GA_THREADS = 256, GA_ROWS = 32;
 constexpr int GA_TABLE = 160 * 1024;   // bytes of the table, at most
 
-template <int BITS, typename XT, int TM, int NL>
-__global__ void __launch_bounds__(GA_THREADS) gemv_act_kernel(const GemvArgs p) {
-    constexpr int ROWS = 32 * NL;
-    extern __shared__ __align__(16) uint8_t ga_smem[];
-    __half2* table = reinterpret_cast<__half2*>(ga_smem);   // [ng][ROWS]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const unsigned cta = blockIdx.x / p.split, rank = blockIdx.x % p.split;
-    const long long nc = (long long)(cta % p.nblocks) * ROWS, n0 = nc + NL * lane;
-    const int m0 = (int)(cta / p.nblocks) * TM;
-    const int K = (int)p.K, chunks = K / 8;
-    const XT* X = reinterpret_cast<const XT*>(p.X);
+// The table's entries for the rows from nc on.
+template <int BITS>
+__device__ __forceinline__ void act_table(const GemvArgs& p, __half2* table, long long nc) {
     const long long zwords = (p.N * BITS + 31) / 32;
-
-    for (int e = tid; e < p.ng * ROWS; e += GA_THREADS) {
-        const int gi = e / ROWS;
-        const long long n = nc + e % ROWS;
+    for (int e = threadIdx.x; e < p.ng * GA_ROWS; e += GA_THREADS) {
+        const int gi = e / GA_ROWS;
+        const long long n = nc + e % GA_ROWS;
         __half s = __float2half(0.f);
         uint32_t z = 1u << (BITS - 1);
         if (n < p.N) {
@@ -647,97 +641,32 @@ __global__ void __launch_bounds__(GA_THREADS) gemv_act_kernel(const GemvArgs p) 
         }
         table[e] = __halves2half2(s, __ushort_as_half((unsigned short)(0x6400u | z)));   // 1024 + z
     }
-    __syncthreads();
-
-    // chunks of this CTA, taken by its warps in turn
-    const int c0 = (int)((long long)chunks * rank / p.split), c1 = (int)((long long)chunks * (rank + 1) / p.split);
-    struct Chunk {
-        uint32_t w[2][NL];
-        int4 g[2];
-        XRaw<XT> x[TM];
-    };
-    auto load = [&](int c, Chunk& q) {
-        const int k = 8 * c;
-        const long long r = (long long)k * BITS / 32;
-        // 24 bits from bit 16 or 24 of a word on end in the next
-        const int words = BITS == 8 || (BITS == 3 && ((k * 3) & 31) > 8) ? 2 : 1;
+}
+// The one or two words of the columns k .. k + 7 of four neighbouring rows.
+template <int BITS>
+__device__ __forceinline__ void act_words(const GemvArgs& p, int k, long long n0, uint32_t (&w)[2][4]) {
+    const long long r = (long long)k * BITS / 32;
+    // 24 bits from bit 16 or 24 of a word on end in the next
+    const int words = BITS == 8 || (BITS == 3 && ((k * 3) & 31) > 8) ? 2 : 1;
 #pragma unroll
-        for (int i = 0; i < (BITS == 8 || BITS == 3 ? 2 : 1); ++i) {
-            const int32_t* src = p.qweight + (r + (i < words ? i : 0)) * p.N + n0;
-            if (NL == 4 && p.vec) {
-                const uint4 u = n0 < p.N ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
-                q.w[i][0] = u.x;
-                q.w[i][1 % NL] = u.y;
-                q.w[i][2 % NL] = u.z;
-                q.w[i][3 % NL] = u.w;
-                if (NL == 1) q.w[i][0] = u.x;
-            } else {
+    for (int i = 0; i < (BITS == 8 || BITS == 3 ? 2 : 1); ++i) {
+        const int32_t* src = p.qweight + (r + (i < words ? i : 0)) * p.N + n0;
+        if (p.vec) {
+            const uint4 u = n0 < p.N ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int j = 0; j < NL; ++j) q.w[i][j] = n0 + j < p.N ? (uint32_t)__ldg(src + j) : 0u;
-            }
+            for (int j = 0; j < 4; ++j) w[i][j] = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i][j] = n0 + j < p.N ? (uint32_t)__ldg(src + j) : 0u;
         }
-        if constexpr (BITS < 8 && BITS != 3) {
-#pragma unroll
-            for (int j = 0; j < NL; ++j) q.w[1][j] = 0;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) reinterpret_cast<int*>(q.g)[j] = __ldg(p.g_idx + k + j);
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-            if (m0 + t < p.M) q.x[t] = load_x8(X + (long long)(m0 + t) * K + k);
-    };
-    float acc[TM][NL] = {};
-    Chunk now = {}, next = {};
-    int c = c0 + warp;
-    if (c < c1) load(c, now);
-    for (; c < c1; c += GA_THREADS / 32) {
-        if (c + GA_THREADS / 32 < c1) load(c + GA_THREADS / 32, next);
-        uint32_t nib[NL];
-        if constexpr (BITS <= 4) {
-#pragma unroll
-            for (int j = 0; j < NL; ++j) nib[j] = chunk_nibbles<BITS>(now.w[0][j], now.w[1][j], c & 3);
-        }
-        float x[TM][8];
-#pragma unroll
-        for (int t = 0; t < TM; ++t) x_floats(now.x[t], x[t]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            int gi = reinterpret_cast<const int*>(now.g)[i];
-            if ((unsigned)gi >= (unsigned)p.ng) {
-                if (lane == 0) record_status(GPTQ_ERR_INVALID_ARG, 8ll * c + i);
-                gi = 0;
-            }
-            uint32_t e[NL];
-            if constexpr (NL == 4) {
-                const uint4 u = *reinterpret_cast<const uint4*>(table + gi * ROWS + 4 * lane);
-                e[0] = u.x;
-                e[1] = u.y;
-                e[2] = u.z;
-                e[3] = u.w;
-            } else {
-                e[0] = *reinterpret_cast<const uint32_t*>(table + gi * ROWS + lane);
-            }
-#pragma unroll
-            for (int j = 0; j < NL; ++j) {
-                const uint32_t q = BITS <= 4 ? (nib[j] >> (4 * i)) & 15u : (now.w[i >> 2][j] >> (8 * (i & 3))) & 255u;
-                const float2 sz = __half22float2(as_half2(e[j]));
-                // 0x44800000 | q << 13 is 1024 + q
-                const float w = sz.x * (__uint_as_float(0x44800000u | (q << 13)) - sz.y);
-#pragma unroll
-                for (int t = 0; t < TM; ++t) acc[t][j] = fmaf(x[t][i], w, acc[t][j]);
-            }
-        }
-        now = next;
     }
-
-    // join the warps, then the CTAs of the cluster, in a fixed order
-    __syncthreads();
-    float* sums = reinterpret_cast<float*>(ga_smem);   // [8 warps][TM][ROWS]
-    constexpr int E = TM * ROWS;
-#pragma unroll
-    for (int t = 0; t < TM; ++t)
-#pragma unroll
-        for (int j = 0; j < NL; ++j) sums[warp * E + t * ROWS + NL * lane + j] = acc[t][j];
+}
+// Joins the warps' sums [8][TOK][GA_ROWS], then the CTAs' of the cluster, in a fixed order, and stores.
+template <int TOK>
+__device__ __forceinline__ void act_join(const GemvArgs& p, float* sums, long long nc, int m0, unsigned rank) {
+    constexpr int ROWS = GA_ROWS, E = TOK * ROWS;
+    const int tid = threadIdx.x;
     __syncthreads();
     auto finish = [&](int e, float y) {
         const int m = m0 + e / ROWS;
@@ -761,6 +690,122 @@ __global__ void __launch_bounds__(GA_THREADS) gemv_act_kernel(const GemvArgs p) 
         __syncwarp();
         cluster_sync_all();   // no CTA leaves while its sums are being read
     }
+}
+
+// Pairs (i, i + 4) of a thread's columns as bf16, which holds e4m3 exactly.
+template <typename XT>
+__device__ __forceinline__ void x_pairs_bf16(const XRaw<XT>& r, uint32_t (&b)[4]) {
+    if constexpr (sizeof(XT) == 2) {
+        x_pairs<false>(r, b);
+    } else {
+        float x[8];
+        x_floats(r, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = bits_of(__floats2bfloat162_rn(x[i], x[i + 4]));
+    }
+}
+
+template <int BITS, typename XT, int MT>
+__global__ void __launch_bounds__(GA_THREADS, MT == 1 ? 3 : 2) gemv_act_kernel(const GemvArgs p) {
+    constexpr int ROWS = GA_ROWS, TOK = 8 * MT, PARTS = BITS == 8 ? 3 : 2, E = TOK * ROWS;
+    extern __shared__ __align__(16) uint8_t ga_smem[];
+    __half2* table = reinterpret_cast<__half2*>(ga_smem);   // [ng][ROWS]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
+    const unsigned cta = blockIdx.x / p.split, rank = blockIdx.x % p.split;
+    const long long nc = (long long)(cta % p.nblocks) * ROWS, n0 = nc + 4 * gid;
+    const int m0 = (int)(cta / p.nblocks) * TOK;
+    const int K = (int)p.K, steps = (K + 31) / 32;
+    const XT* X = reinterpret_cast<const XT*>(p.X);
+    act_table<BITS>(p, table, nc);
+    __syncthreads();
+
+    const int s0 = (int)((long long)steps * rank / p.split), s1 = (int)((long long)steps * (rank + 1) / p.split);
+    struct Chunk {
+        uint32_t w[2][4];
+        int g[8];
+        XRaw<XT> x[MT];
+    };
+    auto load = [&](int st, Chunk& q) {   // columns k .. k + 7; none behind the last
+        const int k = 32 * st + 8 * tig;
+        q = Chunk{};
+        if (k >= K) return;
+        act_words<BITS>(p, k, n0, q.w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q.g[j] = __ldg(p.g_idx + k + j);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            if (m0 + 8 * mt + gid < p.M) q.x[mt] = load_x8(X + (long long)(m0 + 8 * mt + gid) * K + k);
+    };
+    float sum[2][MT][4] = {};   // tile j: rows n0 + j and n0 + j + 2
+    Chunk now = {}, next = {};
+    int st = s0 + warp;
+    if (st < s1) load(st, now);
+    for (; st < s1; st += GA_THREADS / 32) {
+        if (st + GA_THREADS / 32 < s1) load(st + GA_THREADS / 32, next);
+        const bool in = 32 * st + 8 * tig < K;
+        uint32_t nib[4];
+        if constexpr (BITS <= 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) nib[j] = chunk_nibbles<BITS>(now.w[0][j], now.w[1][j], tig);
+        }
+        uint32_t xb[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) x_pairs_bf16<XT>(now.x[mt], xb[mt]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // pairs (i, i + 4) of columns, i = 2 h and 2 h + 1
+            uint32_t a[PARTS][4][2];
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+                const int i = 2 * h + i2;
+                uint4 e[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    int gi = now.g[i + 4 * t];
+                    if ((unsigned)gi >= (unsigned)p.ng) {
+                        if (gid == 0) record_status(GPTQ_ERR_INVALID_ARG, 32ll * st + 8 * tig + i + 4 * t);
+                        gi = 0;
+                    }
+                    e[t] = *reinterpret_cast<const uint4*>(table + gi * ROWS + 4 * gid);
+                }
+                const uint32_t e0[4] = {e[0].x, e[0].y, e[0].z, e[0].w}, e1[4] = {e[1].x, e[1].y, e[1].z, e[1].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t q0 = BITS <= 4 ? nib[j] >> (4 * i) & 15u : now.w[0][j] >> (8 * i) & 255u;
+                    const uint32_t q1 = BITS <= 4 ? nib[j] >> (4 * i + 16) & 15u : now.w[1][j] >> (8 * i) & 255u;
+                    const float2 z0 = __half22float2(as_half2(e0[j])), z1 = __half22float2(as_half2(e1[j]));
+                    float w0 = z0.x * (__uint_as_float(0x44800000u | (q0 << 13)) - z0.y);
+                    float w1 = z1.x * (__uint_as_float(0x44800000u | (q1 << 13)) - z1.y);
+#pragma unroll
+                    for (int c = 0; c < PARTS; ++c) {
+                        const uint32_t u = bits_of(__floats2bfloat162_rn(w0, w1));
+                        a[c][j][i2] = in ? u : 0u;
+                        w0 -= __uint_as_float(u << 16);
+                        w1 -= __uint_as_float(u & 0xFFFF0000u);
+                    }
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < PARTS; ++c)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        mma_16816(sum[j][mt], a[c][j][0], a[c][j + 2][0], a[c][j][1], a[c][j + 2][1], xb[mt][2 * h],
+                                  xb[mt][2 * h + 1], __nv_bfloat16());
+        }
+        now = next;
+    }
+
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ga_smem);   // [8 warps][TOK][ROWS]
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sums[warp * E + (8 * mt + 2 * tig + (c & 1)) * ROWS + 4 * gid + j + (c & 2)] = sum[j][mt][c];
+    act_join<TOK>(p, sums, nc, m0, rank);
 }
 
 }  // namespace gq
@@ -830,22 +875,23 @@ cudaError_t gemv_mma_run(const gq::GemvArgs& p, cudaStream_t st) {
     return gemv_mma_launch<BITS, XT, 4, 4>(p, st);
 }
 
-template <int BITS, typename XT, int TM, int NL>
+template <int BITS, typename XT, int MT>
 cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
-    constexpr int ROWS = 32 * NL;
-    constexpr auto kern = gq::gemv_act_kernel<BITS, XT, TM, NL>;
+    constexpr int TOK = 8 * MT, ROWS = gq::GA_ROWS;
+    constexpr auto kern = gq::gemv_act_kernel<BITS, XT, MT>;
     GQ_TRY((smem_attr_once<kern, gq::GA_TABLE>()));
     p.nblocks = (unsigned)((p.N + ROWS - 1) / ROWS);
     p.vec = p.N % 4 == 0;
-    const long long blocks = (long long)p.nblocks * ((p.M + TM - 1) / TM);
-    // K is split until there are two CTAs to an SM, with four chunks at least for each warp
+    const long long blocks = (long long)p.nblocks * ((p.M + TOK - 1) / TOK);
+    // K is split until there is a CTA to an SM, with 64 columns at least for each warp: every CTA builds
+    // its table, so two to an SM took 44 us where this takes 38 us (2 tokens, 4096 x 11008)
     p.split = 1;
-    while (p.split < 8 && blocks * p.split < 2 * num_sms() && p.K >= 8ll * 32 * 2 * p.split) p.split *= 2;
+    while (p.split < 8 && blocks * p.split < num_sms() && p.K >= 8ll * 32 * 2 * p.split) p.split *= 2;
     if (blocks * p.split > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * p.split));
     cfg.blockDim = dim3(gq::GA_THREADS);
-    cfg.dynamicSmemBytes = std::max((size_t)p.ng * ROWS * 4, (size_t)(gq::GA_THREADS / 32) * TM * ROWS * 4);
+    cfg.dynamicSmemBytes = std::max((size_t)p.ng * ROWS * 4, (size_t)(gq::GA_THREADS / 32) * TOK * ROWS * 4);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -858,16 +904,13 @@ cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
     return e;
 }
 
-// True where the table of gemv_act_kernel fits; the launch's status is then in *e.  Two tokens at a time
-// up to M = 2, for fewer registers and more CTAs on an SM.
+// True where the table of gemv_act_kernel fits; the launch's status is then in *e.
 template <int BITS, typename XT>
 bool gemv_act_run(const gq::GemvArgs& p, cudaStream_t st, cudaError_t* e) {
-    if ((long long)p.ng * 128 * 4 <= gq::GA_TABLE)
-        *e = p.M <= 2 ? gemv_act_launch<BITS, XT, 2, 4>(p, st) : gemv_act_launch<BITS, XT, 8, 4>(p, st);
-    else if ((long long)p.ng * 32 * 4 <= gq::GA_TABLE)
-        *e = p.M <= 2 ? gemv_act_launch<BITS, XT, 2, 1>(p, st) : gemv_act_launch<BITS, XT, 8, 1>(p, st);
-    else
-        return false;
+    if ((long long)p.ng * gq::GA_ROWS * 4 > gq::GA_TABLE) return false;
+    *e = p.M <= 8    ? gemv_act_launch<BITS, XT, 1>(p, st)
+         : p.M <= 16 ? gemv_act_launch<BITS, XT, 2>(p, st)
+                     : gemv_act_launch<BITS, XT, 4>(p, st);
     return true;
 }
 
