@@ -5,7 +5,7 @@
 // with g(k) = k / g, or g_idx[k] for layers quantized in activation order.  X is bf16 (xs = 1)
 // or e4m3 with one fp32 scale per row.
 //
-// Three kernels:
+// Two kernels:
 //
 // gemv_mma_kernel (groups of consecutive columns).  The work is one pass over the packed words, so
 // the design is about issue slots next to the loads: with fp32 FMAs every weight costs an unpack, a
@@ -29,9 +29,7 @@
 // that: the time is instruction issue and the fixed cost of a stage (a barrier to pass, scales, a flush
 // per group).
 //
-// gemv_act_kernel (g_idx: any column in any group; see there), and gemv_lane_kernel for layers with so
-// many groups that its table does not fit (above 1280): one lane per row n, eight warps split the columns,
-// latency-bound and meant for correctness alone.
+// gemv_act_kernel (g_idx: any column in any group): see there.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -41,10 +39,6 @@
 #include "pack.cuh"
 
 namespace gq {
-
-__device__ __forceinline__ float to_float(const __nv_bfloat16& v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(const float& v) { return v; }
-__device__ __forceinline__ float to_float(const __nv_fp8_e4m3& v) { return (float)v; }
 
 struct GemvArgs {
     const void* X;            // [M, K]
@@ -66,57 +60,6 @@ struct GemvArgs {
     int tma;                  // words and X by TMA
     int gshift;               // log2 g, or 31 for one group per row
 };
-
-constexpr int GV_WARPS = 8, GV_TOK = 4;
-
-template <typename XT>
-__global__ void __launch_bounds__(32 * GV_WARPS) gemv_lane_kernel(const GemvArgs p) {
-    __shared__ float part[GV_WARPS][GV_TOK][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long n = (long long)(blockIdx.x % p.nblocks) * 32 + lane;
-    const int m0 = (int)(blockIdx.x / p.nblocks) * GV_TOK;
-    const long long zwords = (p.N * p.bits + 31) / 32;
-    const long long run = (p.K + GV_WARPS - 1) / GV_WARPS;
-    const long long k0 = warp * run, k1 = min(p.K, k0 + run);
-    const XT* X = reinterpret_cast<const XT*>(p.X);
-    float acc[GV_TOK] = {};
-    if (n < p.N) {
-        long long have = -1;
-        float s = 0.f, z = (float)(1 << (p.bits - 1));
-        for (long long k = k0; k < k1; ++k) {
-            long long gi = p.g_idx ? p.g_idx[k] : k / p.g;
-            if (gi < 0 || gi >= p.ng) {
-                record_status(GPTQ_ERR_INVALID_ARG, k);
-                gi = 0;
-            }
-            if (gi != have) {
-                have = gi;
-                s = __half2float(p.scales[gi * p.N + n]);
-                if (p.qzeros) z = (float)stream_code(p.qzeros + gi * zwords, 1, n, p.bits);
-            }
-            const float w = s * ((float)stream_code(p.qweight + n, p.N, k, p.bits) - z);
-#pragma unroll
-            for (int t = 0; t < GV_TOK; ++t)
-                if (m0 + t < p.M) acc[t] = fmaf(to_float(X[(long long)(m0 + t) * p.K + k]), w, acc[t]);
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < GV_TOK; ++t) part[warp][t][lane] = acc[t];
-    __syncthreads();
-    if (warp < GV_TOK && m0 + warp < p.M && n < p.N) {
-        float y = 0.f;
-#pragma unroll
-        for (int w = 0; w < GV_WARPS; ++w) y += part[w][warp][lane];
-        const int m = m0 + warp;
-        if (p.x_scale) y *= p.x_scale[m];
-        const long long at = (long long)m * p.N + n;
-        if (p.y_bf16)
-            reinterpret_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(y);
-        else
-            reinterpret_cast<float*>(p.Y)[at] = y;
-    }
-}
-
 
 // ---------------------------------------------------------------------------- tensor instruction
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -621,8 +564,9 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
 // for codes of up to 4 bits, three for 8 bits), so the products are exact and the sums fp32, and a
 // weight's decoding and cutting, some 14 instructions, serve up to 32 tokens.
 // Bound by instruction issue: 4096 x 11008, 4-bit groups of 128, 2 tokens 38 us, 16 tokens 42 us, 64
-// tokens in two tiles 105 us.  fp32 multiply-adds in place of the tensor instruction took 39 us for 2
-// tokens and 119 us for 8; lookups in global memory (gemv_lane_kernel) 436 us for 2.
+// tokens in two tiles 96 us.  fp32 multiply-adds in place of the tensor instruction took 39 us for 2
+// tokens and 119 us for 8.  Where the table does not fit (above 1280 groups), TABLE is false and every
+// weight's entry is read from global memory.
 constexpr int GA_THREADS = 256, GA_ROWS = 32;
 constexpr int GA_TABLE = 160 * 1024;   // bytes of the table, at most
 
@@ -661,6 +605,22 @@ __device__ __forceinline__ void act_words(const GemvArgs& p, int k, long long n0
             for (int j = 0; j < 4; ++j) w[i][j] = n0 + j < p.N ? (uint32_t)__ldg(src + j) : 0u;
         }
     }
+}
+// Entries of a group for the rows n0 .. n0 + 3, as the table holds them.
+template <int BITS>
+__device__ __forceinline__ uint4 act_entries(const GemvArgs& p, int gi, long long n0) {
+    const long long zwords = (p.N * BITS + 31) / 32;
+    uint32_t e[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t s = 0, z = 1u << (BITS - 1);
+        if (n0 + j < p.N) {
+            s = __half_as_ushort(p.scales[(long long)gi * p.N + n0 + j]);
+            if (p.qzeros != nullptr) z = stream_code(p.qzeros + gi * zwords, 1, n0 + j, BITS);
+        }
+        e[j] = s | (0x6400u | z) << 16;   // 1024 + z
+    }
+    return make_uint4(e[0], e[1], e[2], e[3]);
 }
 // Joins the warps' sums [8][TOK][GA_ROWS], then the CTAs' of the cluster, in a fixed order, and stores.
 template <int TOK>
@@ -705,7 +665,7 @@ __device__ __forceinline__ void x_pairs_bf16(const XRaw<XT>& r, uint32_t (&b)[4]
     }
 }
 
-template <int BITS, typename XT, int MT>
+template <int BITS, typename XT, int MT, bool TABLE>
 __global__ void __launch_bounds__(GA_THREADS, MT == 1 ? 3 : 2) gemv_act_kernel(const GemvArgs p) {
     constexpr int ROWS = GA_ROWS, TOK = 8 * MT, PARTS = BITS == 8 ? 3 : 2, E = TOK * ROWS;
     extern __shared__ __align__(16) uint8_t ga_smem[];
@@ -716,7 +676,7 @@ __global__ void __launch_bounds__(GA_THREADS, MT == 1 ? 3 : 2) gemv_act_kernel(c
     const int m0 = (int)(cta / p.nblocks) * TOK;
     const int K = (int)p.K, steps = (K + 31) / 32;
     const XT* X = reinterpret_cast<const XT*>(p.X);
-    act_table<BITS>(p, table, nc);
+    if (TABLE) act_table<BITS>(p, table, nc);
     __syncthreads();
 
     const int s0 = (int)((long long)steps * rank / p.split), s1 = (int)((long long)steps * (rank + 1) / p.split);
@@ -765,7 +725,8 @@ __global__ void __launch_bounds__(GA_THREADS, MT == 1 ? 3 : 2) gemv_act_kernel(c
                         if (gid == 0) record_status(GPTQ_ERR_INVALID_ARG, 32ll * st + 8 * tig + i + 4 * t);
                         gi = 0;
                     }
-                    e[t] = *reinterpret_cast<const uint4*>(table + gi * ROWS + 4 * gid);
+                    e[t] = TABLE ? *reinterpret_cast<const uint4*>(table + gi * ROWS + 4 * gid)
+                                 : act_entries<BITS>(p, gi, n0);
                 }
                 const uint32_t e0[4] = {e[0].x, e[0].y, e[0].z, e[0].w}, e1[4] = {e[1].x, e[1].y, e[1].z, e[1].w};
 #pragma unroll
@@ -875,10 +836,10 @@ cudaError_t gemv_mma_run(const gq::GemvArgs& p, cudaStream_t st) {
     return gemv_mma_launch<BITS, XT, 4, 4>(p, st);
 }
 
-template <int BITS, typename XT, int MT>
+template <int BITS, typename XT, int MT, bool TABLE>
 cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
     constexpr int TOK = 8 * MT, ROWS = gq::GA_ROWS;
-    constexpr auto kern = gq::gemv_act_kernel<BITS, XT, MT>;
+    constexpr auto kern = gq::gemv_act_kernel<BITS, XT, MT, TABLE>;
     GQ_TRY((smem_attr_once<kern, gq::GA_TABLE>()));
     p.nblocks = (unsigned)((p.N + ROWS - 1) / ROWS);
     p.vec = p.N % 4 == 0;
@@ -891,7 +852,7 @@ cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * p.split));
     cfg.blockDim = dim3(gq::GA_THREADS);
-    cfg.dynamicSmemBytes = std::max((size_t)p.ng * ROWS * 4, (size_t)(gq::GA_THREADS / 32) * TOK * ROWS * 4);
+    cfg.dynamicSmemBytes = std::max(TABLE ? (size_t)p.ng * ROWS * 4 : 0, (size_t)(gq::GA_THREADS / 32) * TOK * ROWS * 4);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -904,14 +865,12 @@ cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
     return e;
 }
 
-// True where the table of gemv_act_kernel fits; the launch's status is then in *e.
 template <int BITS, typename XT>
-bool gemv_act_run(const gq::GemvArgs& p, cudaStream_t st, cudaError_t* e) {
-    if ((long long)p.ng * gq::GA_ROWS * 4 > gq::GA_TABLE) return false;
-    *e = p.M <= 8    ? gemv_act_launch<BITS, XT, 1>(p, st)
-         : p.M <= 16 ? gemv_act_launch<BITS, XT, 2>(p, st)
-                     : gemv_act_launch<BITS, XT, 4>(p, st);
-    return true;
+cudaError_t gemv_act_run(const gq::GemvArgs& p, cudaStream_t st) {
+    if ((long long)p.ng * gq::GA_ROWS * 4 > gq::GA_TABLE) return gemv_act_launch<BITS, XT, 1, false>(p, st);
+    if (p.M <= 8) return gemv_act_launch<BITS, XT, 1, true>(p, st);
+    if (p.M <= 16) return gemv_act_launch<BITS, XT, 2, true>(p, st);
+    return gemv_act_launch<BITS, XT, 4, true>(p, st);
 }
 
 template <typename XT>
@@ -925,17 +884,12 @@ cudaError_t gemv_run_x(gq::GemvArgs p, cudaStream_t st) {
             default: return gemv_mma_run<8, XT>(p, st);
         }
     }
-    cudaError_t e;
     switch (p.bits) {
-        case 2: if (gemv_act_run<2, XT>(p, st, &e)) return e; break;
-        case 3: if (gemv_act_run<3, XT>(p, st, &e)) return e; break;
-        case 4: if (gemv_act_run<4, XT>(p, st, &e)) return e; break;
-        default: if (gemv_act_run<8, XT>(p, st, &e)) return e; break;
+        case 2: return gemv_act_run<2, XT>(p, st);
+        case 3: return gemv_act_run<3, XT>(p, st);
+        case 4: return gemv_act_run<4, XT>(p, st);
+        default: return gemv_act_run<8, XT>(p, st);
     }
-    p.nblocks = (unsigned)((p.N + 31) / 32);
-    const long long blocks = (long long)p.nblocks * ((p.M + gq::GV_TOK - 1) / gq::GV_TOK);
-    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    return launch_plain(gq::gemv_lane_kernel<XT>, dim3((unsigned)blocks), dim3(32 * gq::GV_WARPS), 0, st, p);
 }
 
 inline cudaError_t gemv_run(const gq::GemvArgs& p, bool x_e4m3, cudaStream_t st) {

@@ -138,6 +138,8 @@ GEMV = [
     (33, 44, 520, 2, 64, False, 1, "e4m3", "f32"),
     (64, 70, 16384, 4, 16, False, 1, "bf16", "f32"),   # 1024 groups
     (3, 36, 32768, 4, 16, False, 1, "e4m3", "f32"),    # 2048 groups: no table
+    (17, 133, 65536, 3, 32, False, 1, "bf16", "f32"),  # the same, odd rows, several token tiles
+    (9, 24, 24576, 8, 16, True, 1, "e4m3", "bf16"),
     (2, 129, 16392, 3, 16, False, 2, "e4m3", "bf16"),
     (9, 300, 1032, 3, 32, False, 1, "bf16", "f32"),
 ]
