@@ -35,10 +35,10 @@
 //
 // What bounds it: each 128-column K tile takes about 900 clocks, of which the MMAs are 520 (eight of
 // 65 clocks) and an epilogue warp and a converter set are busy for most of it.  Neither leaving out the
-// code conversion (-3 %), the multiplications by s_g (-6 %) nor the second MMA pass (-9 %) changes it
+// code conversion (-4 %), the multiplications by s_g (-7 %) nor the second MMA pass (-10 %) changes it
 // much, nor a third converter set, nor a ring of six A operands with two accumulators: the roles'
 // latencies (a passed barrier is 100-200 clocks) are close to each other.  4-bit groups of 128:
-// 2048 tokens x 4096 x 4096 in 72 us (950 TFLOP/s), 8192 tokens x 11008 x 4096 in 647 us
+// 2048 tokens x 4096 x 4096 in 73 us (940 TFLOP/s), 8192 tokens x 11008 x 4096 in 650 us
 // (1140 TFLOP/s, 35 % of the 8-bit rate); groups of 32 take 174 us for the former, as every group is an
 // accumulator to drain.
 //
@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset, so that accesses stay shared-memory ones
     uint8_t* par = smem + STAGES * Cfg::STAGE_BYTES;   // [PST] scales [4][128] fp16, zero points [4][16] words
-    float* xs = reinterpret_cast<float*>(par + D8_PST * (D8_PAR_S + D8_PAR_Z));   // [2][TT] scales of the tokens of this tile and the next
+    // [2][TT] scales of the tokens of this tile and the next
+    float* xs = reinterpret_cast<float*>(par + D8_PST * (D8_PAR_S + D8_PAR_Z));
     uint64_t* full = reinterpret_cast<uint64_t*>(xs + 2 * TT);   // [STAGES] TMA landed
     uint64_t* empty = full + STAGES;                         // [STAGES] MMAs of the stage done
     uint64_t* conv = empty + STAGES;                         // [AST] A operand written
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
     uint64_t* dfull = aempty + D8_AST;                       // [ND] segment complete
     uint64_t* dempty = dfull + ND;                        // [ND] segment drained
     uint64_t* pfull = dempty + ND;                        // [PST] scales and zero points landed
-    uint64_t* pempty = pfull + D8_PST;                       // [PST] scales read by the epilogue's warps, zero points used
+    uint64_t* pempty = pfull + D8_PST;                       // [PST] scales and zero points used
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pempty + D8_PST);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -642,7 +643,7 @@ cudaError_t dq_gemm_e4m3_launch(const uint8_t* X8, const int32_t* qweight, gq::D
     return e;
 }
 
-// Up to 64 tokens a tile of 64: 64 x 4096 x 4096 took 11.9 us against 15.8 us padded to 128.
+// Up to 64 tokens a tile of 64: 64 x 4096 x 4096 takes 11.0 us, 128 tokens in a tile of 128 13.3 us.
 template <int BITS>
 cudaError_t dq_gemm_e4m3_run(const uint8_t* X8, const int32_t* qweight, const gq::D8Args& p, cudaStream_t st) {
     if (p.M <= 64) return dq_gemm_e4m3_launch<BITS, 64>(X8, qweight, p, st);

@@ -22,10 +22,10 @@
 // sums, and those of the CTAs of a cluster that split K, are joined in a fixed order through shared
 // memory.
 //
-// Measured, packed words from memory: 4-bit groups of 128, one token through 4096 x 4096 7.5 us (8.9 MB,
-// 1.2 TB/s: of that about 3 us are launch, first loads and the join), through 11008 x 4096 14.5 us; eight
+// Measured, packed words from memory: 4-bit groups of 128, one token through 4096 x 4096 7.7 us (8.9 MB,
+// 1.1 TB/s: of that about 4.6 us are launch, first loads and the join), through 11008 x 4096 14.7 us; eight
 // e4m3 tokens through 50001 x 8192 (odd row count: bulk copies of rows) 101 us (214 MB, 2.1 TB/s); 16
-// tokens through 11008 x 4096, 3 bits, groups of 64, 34 us.  The copies alone would take a third of
+// tokens through 11008 x 4096, 3 bits, groups of 64, 31 us.  The copies alone would take a third of
 // that: the time is instruction issue and the fixed cost of a stage (a barrier to pass, scales, a flush
 // per group).
 //
@@ -227,7 +227,8 @@ constexpr int GM_WARPS = 8;        // four of 32 rows n each, times two runs of 
 constexpr int GM_THREADS = 32 * GM_WARPS + 32;   // and one that fills the ring
 constexpr int GM_ROWS = 128;       // rows n of a CTA
 constexpr int GM_K = 256;          // columns of a stage, 128 for each half of the warps
-constexpr int GM_WSTRIDE = 4 * GM_ROWS + 32;   // bytes of a row of words: 16-byte reads without bank conflicts, room to skew
+// bytes of a row of words: 16-byte reads without bank conflicts, room to skew
+constexpr int GM_WSTRIDE = 4 * GM_ROWS + 32;
 
 template <int BITS, typename XT, int MT, int GROUPS>
 struct GmCfg {
