@@ -9,9 +9,10 @@
 // maximum per row suffice, and they are taken together.  |v| is compared by its bit pattern,
 // whose order is that of the magnitudes with NaN above infinity, so a NaN reaches x_scale.
 //
-// Bound by memory for many rows: 2048 x 4096 bf16 with residual 12 us (58.7 MB, 4.7 TB/s; of it about
-// 2 us launch and tail), 8192 rows 37 us (6.3 TB/s), 4096 x 11008 bf16 without norm 28 us (4.8 TB/s),
-// 8191 x 16384 fp32 138 us (4.9 TB/s, w re-read from L2 for every row); by latency for few: 2.0 us for one row to 64.
+// Bound by memory for many rows: 2048 x 4096 bf16 with residual 13 us (58.7 MB, 4.4 TB/s; of it about
+// 2.5 us launch and tail), 8192 rows 39 us (6.0 TB/s), 4096 x 11008 bf16 without norm 28 us (4.8 TB/s),
+// 8191 x 16384 fp32 138 us (4.9 TB/s, w re-read from L2 for every row); by latency for few: 2.4 us for one
+// row, 2.8 us for 64.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -152,7 +153,6 @@ __host__ __device__ constexpr int rw_max_threads(int vec) { return vec <= 2 ? 10
 // R' may be X or R: a thread writes only elements that it has read itself.
 template <typename XT, typename WT, bool NORM, int VEC>
 __global__ void __launch_bounds__(rw_max_threads(VEC)) rows_e4m3_kernel(const RowsArgs p) {
-    pdl_wait();
     const bool wr = p.warp_rows != 0;
     const long long row = wr ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= p.M) return;   // whole warps
@@ -212,7 +212,6 @@ __global__ void __launch_bounds__(rw_max_threads(VEC)) rows_e4m3_kernel(const Ro
 // element has read its X and R.
 template <typename XT, typename WT, bool NORM>
 __global__ void __launch_bounds__(1024) rows_e4m3_long_kernel(const RowsArgs p) {
-    pdl_wait();
     const long long row = blockIdx.x;
     const XT* X = reinterpret_cast<const XT*>(p.X) + row * p.D;
     const XT* R = p.R ? reinterpret_cast<const XT*>(p.R) + row * p.D : nullptr;
@@ -270,8 +269,9 @@ cudaError_t rows_e4m3_run(gq::RowsArgs p, long long M, const char* name, cudaStr
     dim3 grid((unsigned)M);
     const int vecs = (int)(p.D / 8);
     p.M = M;
+    // Ordinary launches: what precedes a public call may be anything, a wait for another stream included.
     if (vecs > gq::RW_MAX_VECS)
-        return launch_pdl(gq::rows_e4m3_long_kernel<XT, WT, NORM>, grid, dim3(1024), 0, st, p);
+        return launch_plain(gq::rows_e4m3_long_kernel<XT, WT, NORM>, grid, dim3(1024), 0, st, p);
     // Few rows: a vector a thread, for latency.  Many rows: four, for bytes in flight and cheap barriers;
     // eight for long rows without R, whose registers they leave enough of (4096 x 11008 bf16: 28 us against
     // 32 us with four; with R they do not: 2048 x 11008 took 37 us against 29 us).
@@ -286,10 +286,10 @@ cudaError_t rows_e4m3_run(gq::RowsArgs p, long long M, const char* name, cudaStr
         grid.x = (unsigned)((M + 7) / 8);
     }
     switch (vec) {
-        case 1: return launch_pdl(gq::rows_e4m3_kernel<XT, WT, NORM, 1>, grid, dim3(threads), 0, st, p);
-        case 2: return launch_pdl(gq::rows_e4m3_kernel<XT, WT, NORM, 2>, grid, dim3(threads), 0, st, p);
-        case 4: return launch_pdl(gq::rows_e4m3_kernel<XT, WT, NORM, 4>, grid, dim3(threads), 0, st, p);
-        default: return launch_pdl(gq::rows_e4m3_kernel<XT, WT, NORM, 8>, grid, dim3(threads), 0, st, p);
+        case 1: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 1>, grid, dim3(threads), 0, st, p);
+        case 2: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 2>, grid, dim3(threads), 0, st, p);
+        case 4: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 4>, grid, dim3(threads), 0, st, p);
+        default: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 8>, grid, dim3(threads), 0, st, p);
     }
 }
 
