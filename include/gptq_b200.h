@@ -291,7 +291,8 @@ gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale
  *   X8       device [M, d_in] e4m3 bytes;  x_scale device fp32 [M].
  * h, the sum and the maximum are fp32: y comes from the unrounded h.  A row whose y is all zero
  * gets x_scale 0 and zero codes.  A row with a NaN or an infinity gets a non-finite x_scale (its
- * products are then non-finite) and leaves the others alone.  Magnitudes of h below 2^60.
+ * products are then non-finite) and leaves the others alone.  Finite rows of any magnitude and any
+ * eps >= 0, as far as h and h weight are neither infinite nor subnormal in fp32.
  * Requires d_in % 8 == 0, d_in <= 65536; X8 8-byte, the other arrays 16-byte aligned (x_scale 4). */
 gptq_status gptq_rms_norm_e4m3(const void* X, const void* residual, gptq_dtype xt, const void* weight, gptq_dtype wt,
                                int64_t M, int64_t d_in, float eps, uint8_t* X8, float* x_scale, void* residual_out,

@@ -9,10 +9,10 @@
 // maximum per row suffice, and they are taken together.  |v| is compared by its bit pattern,
 // whose order is that of the magnitudes with NaN above infinity, so a NaN reaches x_scale.
 //
-// Bound by memory for many rows: 2048 x 4096 bf16 with residual 13 us (58.7 MB, 4.4 TB/s; of it about
-// 2.5 us launch and tail), 8192 rows 39 us (6.0 TB/s), 4096 x 11008 bf16 without norm 28 us (4.8 TB/s),
-// 8191 x 16384 fp32 138 us (4.9 TB/s, w re-read from L2 for every row); by latency for few: 2.4 us for one
-// row, 2.8 us for 64.
+// Bound by memory for many rows: 2048 x 4096 bf16 with residual 12 us (58.7 MB, 4.9 TB/s; of it about
+// 2.5 us launch and tail), 8192 rows 37.6 us (6.2 TB/s), 4096 x 11008 bf16 without norm 28 us (4.8 TB/s),
+// 8191 x 16384 fp32 122 us (5.5 TB/s); by latency for few: 2.4 us for one row, 2.7 us for 64.  Long rows
+// (512 x 65536 bf16 with residual) take 63 us; without the code for sums that fp32 does not hold, 57 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -101,6 +101,72 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], const RowScale& s) 
     return make_uint2(r[0], r[1]);
 }
 
+// A row's sum of squares where fp32 may not hold it.  Where a thread's running sum ``mid`` leaves
+// [2^-100, 2^110] (values from about 2^55 on, or below 2^-50 alone) its values so far go into ``far``
+// instead, scaled by a power of two: positive, the sum of (2^-76 h)^2; or negative, the sum of (2^90 h)^2,
+// which one large value makes negligible.  Both hold the squares of every fp32 value, for any row length here.
+struct SquareSum {
+    float mid = 0.f, far = 0.f;
+    template <int N>
+    __device__ __forceinline__ void add(const float (*h)[8]) {
+        const float before = mid;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {   // N chains side by side
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = fmaf(h[i][j], h[i][j], s);
+            mid += s;
+        }
+        if (!(mid >= 0x1p-100f && mid <= 0x1p110f)) {   // a NaN as well
+            const bool low = mid < 0x1p-100f;
+            const float by = low ? 0x1p90f : 0x1p-76f;
+            float s = before * by * by;
+#pragma unroll
+            for (int i = 0; i < 8 * N; ++i) {
+                const float t = h[i >> 3][i & 7] * by;
+                s = fmaf(t, t, s);
+            }
+            if (low)
+                far = far <= 0.f ? far - s : far;   // a NaN stays
+            else
+                far = far <= 0.f ? s : far + s;
+            mid = 0.f;
+        }
+    }
+    // Adds up the warp's lanes.
+    __device__ __forceinline__ void join() {
+        float high = far <= 0.f ? 0.f : far, low = fminf(far, 0.f);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            mid += __shfl_xor_sync(~0u, mid, o);
+            high += __shfl_xor_sync(~0u, high, o);
+            low += __shfl_xor_sync(~0u, low, o);
+        }
+        far = high != 0.f ? high : low;
+    }
+    // The same over the block.
+    __device__ __forceinline__ void join_block() {
+        __shared__ float s_parts[2][32];
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+        if (lane == 0) {
+            s_parts[0][warp] = mid;
+            s_parts[1][warp] = far;
+        }
+        __syncthreads();
+        mid = lane < warps ? s_parts[0][lane] : 0.f;
+        far = lane < warps ? s_parts[1][lane] : 0.f;
+        join();
+    }
+    // a / (448 sqrt(sum / D + eps)).  The factors of two are shared out so that nothing leaves the range of fp32.
+    __device__ __forceinline__ float scale(float a, float D, float eps) const {
+        if (!(far <= 0.f))   // mid is nothing to it
+            return a * 0x1p-45f / 448.f * rsqrtf(far / D + eps * 0x1p-76f * 0x1p-76f) * 0x1p-31f;
+        if (far < 0.f && mid < 0x1p-60f && eps < 0x1p-60f)
+            return a * 0x1p45f / 448.f * rsqrtf((mid * 0x1p90f * 0x1p90f - far) / D + eps * 0x1p90f * 0x1p90f) * 0x1p45f;
+        return rsqrtf(mid / D + eps) * (a / 448.f);   // far is nothing to mid or eps
+    }
+};
+
 // Joins the threads' sums and maxima over the warp or the block (up to 1024 threads), the same bits on
 // every run.
 template <bool NORM>
@@ -127,20 +193,25 @@ __device__ __forceinline__ void rows_join(float& sum, uint32_t& top, bool warp_o
         top = max(top, __shfl_xor_sync(~0u, top, o));
     }
 }
+// Whether fp32 did not hold the row's sum: too large, or too small beside eps (a NaN as well).
+__device__ __forceinline__ bool sum_lost(float sum, float eps) {
+    return !(fmaxf(sum, eps) >= 0x1p-60f && sum <= 0x1p120f);
+}
 
-template <bool NORM>
-__device__ __forceinline__ RowScale row_scale(const RowsArgs& p, float sum, uint32_t top, float* x_scale, bool first) {
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
     const float a = __uint_as_float(top);
-    if (first) {
-        const float r = NORM ? rsqrtf(sum / (float)p.D + p.eps) : 1.f;
-        *x_scale = a == 0.f ? 0.f : r * (a / 448.f);
-    }
     // a below 2^-100 would overflow 448 / a: the row is lifted by 2^64 first, which is exact
     RowScale s;
     s.f = a < 0x1p-100f ? 0x1p64f : 1.f;
     s.hi = a > 0.f ? 448.f / (a * s.f) : (a == 0.f ? 0.f : a);
     s.lo = a > 0.f && a <= 0x1p100f ? fmaf(-s.hi, a * s.f, 448.f) * (s.hi * (1.f / 448.f)) : 0.f;
     return s;
+}
+
+template <bool NORM>
+__device__ __forceinline__ float x_scale(const RowsArgs& p, const SquareSum& sum, uint32_t top) {
+    const float a = __uint_as_float(top);
+    return a == 0.f ? 0.f : NORM ? sum.scale(a, (float)p.D, p.eps) : a / 448.f;
 }
 
 constexpr int RW_MAX_VECS = 4096;   // vectors of 8 elements in a row of rows_e4m3_kernel, at most
@@ -151,16 +222,23 @@ __host__ __device__ constexpr int rw_max_threads(int vec) { return vec <= 2 ? 10
 // thread, so that X, R and w are read once, the loads of up to four vectors are in flight together, and
 // R' is written before the maximum is known.
 // R' may be X or R: a thread writes only elements that it has read itself.
-template <typename XT, typename WT, bool NORM, int VEC>
-__global__ void __launch_bounds__(rw_max_threads(VEC)) rows_e4m3_kernel(const RowsArgs p) {
+// Rows whose sum fp32 does not hold are read again: from X, or from R', which holds fp32 values exactly.
+// bf16 R' does not and may have replaced X, so with KEEP the values stay in registers until a thread's sum
+// is known to be in range.  RES: there may be an R.  Eight vectors need the registers of both: 8191 x 16384
+// fp32 without R takes 122 us, 151 us with KEEP, 174 us with RES; 1024 x 32768 fp32 with R takes 79 us with
+// KEEP, 90 us without.
+template <typename XT, typename WT, bool NORM, int VEC, bool KEEP, bool RES>
+__global__ void __launch_bounds__(rw_max_threads(VEC), VEC == 1 && sizeof(XT) + sizeof(WT) == 4 ? 2 : 0)
+    rows_e4m3_kernel(const RowsArgs p) {
     const bool wr = p.warp_rows != 0;
     const long long row = wr ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= p.M) return;   // whole warps
     const int t = wr ? threadIdx.x & 31 : threadIdx.x;
     const XT* X = reinterpret_cast<const XT*>(p.X) + row * p.D;
-    const XT* R = p.R ? reinterpret_cast<const XT*>(p.R) + row * p.D : nullptr;
+    const XT* R = RES && p.R ? reinterpret_cast<const XT*>(p.R) + row * p.D : nullptr;
     const int D = (int)p.D, step = wr ? 8 * 32 : 8 * (int)blockDim.x, c0 = 8 * t;
     float v[VEC][8];
+    SquareSum kept;   // KEEP
     float sum = 0.f;
     uint32_t top = 0;
     constexpr int FLIGHT = VEC > 4 ? 4 : VEC;   // vectors of each input in flight
@@ -189,29 +267,52 @@ __global__ void __launch_bounds__(rw_max_threads(VEC)) rows_e4m3_kernel(const Ro
                 for (int j = 0; j < 8; ++j) h[j] += r[i].at(j);
                 if (c0 + (i0 + i) * step < D) store8(reinterpret_cast<XT*>(p.R2) + row * p.D + c0 + (i0 + i) * step, h);
             }
+        }
+        if (NORM && KEEP) kept.add<FLIGHT>(v + i0);
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) {
+            float(&h)[8] = v[i0 + i];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (NORM) {
-                    sum = fmaf(h[j], h[j], sum);
-                    h[j] *= w[i].at(j);
-                }
+                if (NORM && !KEEP) sum = fmaf(h[j], h[j], sum);
+                if (NORM) h[j] *= w[i].at(j);
                 top = max(top, __float_as_uint(h[j]) & 0x7FFFFFFFu);
             }
         }
     }
+    if (KEEP) sum = kept.far == 0.f ? kept.mid : __int_as_float(0x7F800000);   // infinity: not held
     rows_join<NORM>(sum, top, wr);
-    const RowScale s = row_scale<NORM>(p, sum, top, p.x_scale + row, t == 0);
+    const RowScale s = row_scale(top);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const int c = c0 + i * step;
         if (c < D) *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(v[i], s);
     }
+    // x_scale last: a sum that takes longer then holds up no registers
+    SquareSum all{sum, 0.f};
+    if (NORM && (KEEP ? !(sum <= 0x1p120f) : sum_lost(sum, p.eps))) {   // the same for the whole row
+        if (!KEEP) {
+            const XT* H = R ? reinterpret_cast<const XT*>(p.R2) + row * p.D : X;
+            for (int c = c0; c < D; c += step) {
+                Raw8<XT> x;
+                x.load(H + c, true);
+                float h[1][8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[0][j] = x.at(j);
+                kept.add<1>(h);
+            }
+        }
+        kept.join();
+        if (!wr) kept.join_block();
+        all = kept;
+    }
+    if (t == 0) p.x_scale[row] = x_scale<NORM>(p, all, top);
 }
 
 // Rows too long for that: read twice, R' written in the second pass, when the thread that writes an
 // element has read its X and R.
 template <typename XT, typename WT, bool NORM>
-__global__ void __launch_bounds__(1024) rows_e4m3_long_kernel(const RowsArgs p) {
+__global__ void __launch_bounds__(1024, 2) rows_e4m3_long_kernel(const RowsArgs p) {
     const long long row = blockIdx.x;
     const XT* X = reinterpret_cast<const XT*>(p.X) + row * p.D;
     const XT* R = p.R ? reinterpret_cast<const XT*>(p.R) + row * p.D : nullptr;
@@ -219,7 +320,7 @@ __global__ void __launch_bounds__(1024) rows_e4m3_long_kernel(const RowsArgs p) 
     const int D = (int)p.D, step = 8 * (int)blockDim.x;
     float sum = 0.f;
     uint32_t top = 0;
-    float h[8], w[8];
+    float h[1][8], w[8];
     auto load8 = [](const auto* q, float (&to)[8]) {
         Raw8<std::remove_cv_t<std::remove_pointer_t<decltype(q)>>> raw;
         raw.load(q, true);
@@ -227,11 +328,11 @@ __global__ void __launch_bounds__(1024) rows_e4m3_long_kernel(const RowsArgs p) 
         for (int i = 0; i < 8; ++i) to[i] = raw.at(i);
     };
     auto read = [&](int c) {
-        load8(X + c, h);
+        load8(X + c, h[0]);
         if (R) {
             load8(R + c, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] += w[i];
+            for (int i = 0; i < 8; ++i) h[0][i] += w[i];
         }
     };
     for (int c = 8 * (int)threadIdx.x; c < D; c += step) {
@@ -239,22 +340,30 @@ __global__ void __launch_bounds__(1024) rows_e4m3_long_kernel(const RowsArgs p) 
         if (NORM) load8(W + c, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (NORM) sum = fmaf(h[i], h[i], sum);
-            top = max(top, __float_as_uint(NORM ? h[i] * w[i] : h[i]) & 0x7FFFFFFFu);
+            if (NORM) sum = fmaf(h[0][i], h[0][i], sum);
+            top = max(top, __float_as_uint(NORM ? h[0][i] * w[i] : h[0][i]) & 0x7FFFFFFFu);
         }
     }
     rows_join<NORM>(sum, top, false);
-    const RowScale s = row_scale<NORM>(p, sum, top, p.x_scale + row, threadIdx.x == 0);
+    const bool lost = NORM && sum_lost(sum, p.eps);   // summed again in the second pass
+    SquareSum all{lost ? 0.f : sum, 0.f};
+    const RowScale s = row_scale(top);
     for (int c = 8 * (int)threadIdx.x; c < D; c += step) {
         read(c);
-        if (R) store8(reinterpret_cast<XT*>(p.R2) + row * p.D + c, h);
+        if (lost) all.add<1>(h);
+        if (R) store8(reinterpret_cast<XT*>(p.R2) + row * p.D + c, h[0]);
         if (NORM) {
             load8(W + c, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] *= w[i];
+            for (int i = 0; i < 8; ++i) h[0][i] *= w[i];
         }
-        *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(h, s);
+        *reinterpret_cast<uint2*>(p.X8 + row * p.D + c) = e4m3x8(h[0], s);
     }
+    if (lost) {
+        all.join();
+        all.join_block();
+    }
+    if (threadIdx.x == 0) p.x_scale[row] = x_scale<NORM>(p, all, top);
 }
 
 }  // namespace gq
@@ -285,11 +394,15 @@ cudaError_t rows_e4m3_run(gq::RowsArgs p, long long M, const char* name, cudaStr
         threads = 256;
         grid.x = (unsigned)((M + 7) / 8);
     }
+    constexpr bool KEEP = NORM && sizeof(XT) == 2;
+    dim3 block(threads);
     switch (vec) {
-        case 1: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 1>, grid, dim3(threads), 0, st, p);
-        case 2: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 2>, grid, dim3(threads), 0, st, p);
-        case 4: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 4>, grid, dim3(threads), 0, st, p);
-        default: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 8>, grid, dim3(threads), 0, st, p);
+        case 1: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 1, KEEP, NORM>, grid, block, 0, st, p);
+        case 2: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 2, KEEP, NORM>, grid, block, 0, st, p);
+        case 4: return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 4, KEEP, NORM>, grid, block, 0, st, p);
+        default:
+            if (NORM && p.R) return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 8, NORM, NORM>, grid, block, 0, st, p);
+            return launch_plain(gq::rows_e4m3_kernel<XT, WT, NORM, 8, false, false>, grid, block, 0, st, p);
     }
 }
 
