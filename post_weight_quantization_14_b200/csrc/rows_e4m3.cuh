@@ -200,11 +200,12 @@ __device__ __forceinline__ bool sum_lost(float sum, float eps) {
 
 __device__ __forceinline__ RowScale row_scale(uint32_t top) {
     const float a = __uint_as_float(top);
-    // a below 2^-100 would overflow 448 / a: the row is lifted by 2^64 first, which is exact
+    // a below 2^-100 would overflow 448 / a, one above 2^100 would leave lo subnormal: the row is moved by
+    // 2^64 first, which is exact for values that have a code
     RowScale s;
-    s.f = a < 0x1p-100f ? 0x1p64f : 1.f;
+    s.f = a < 0x1p-100f ? 0x1p64f : a > 0x1p100f ? 0x1p-64f : 1.f;
     s.hi = a > 0.f ? 448.f / (a * s.f) : (a == 0.f ? 0.f : a);
-    s.lo = a > 0.f && a <= 0x1p100f ? fmaf(-s.hi, a * s.f, 448.f) * (s.hi * (1.f / 448.f)) : 0.f;
+    s.lo = a > 0.f && a <= 0x1.fffffep127f ? fmaf(-s.hi, a * s.f, 448.f) * (s.hi * (1.f / 448.f)) : 0.f;
     return s;
 }
 

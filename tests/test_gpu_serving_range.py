@@ -73,3 +73,18 @@ def test_rms_norm_rows_that_are_not_finite_stay_marked(d, xt):
     fine = [0, 2, 6, 7, 8]
     y, scale = _rows_reference(Xv[fine], np.ones(d), 0.0)
     _check_rows(X8[fine], xs[fine], y, scale, d)
+
+
+@pytest.mark.parametrize("exp", [-100, -60, 60, 101, 112])
+@pytest.mark.parametrize("M,d", [(3, 64), (400, 4096), (400, 8200), (5, 40000)])
+def test_quantize_boundaries_between_codes_at_any_magnitude(M, d, exp):
+    # as test_quantize_e4m3_boundaries_between_codes: 448 v / a lies on a boundary exactly or far from it
+    rng = np.random.default_rng(M + d + exp + 1000)
+    X, Xv = _tensor(_activations(rng, M, d) * 2.0 ** exp, "bf16")
+    assert np.all(np.isfinite(Xv))
+    X8, xs = torch.empty((M, d), dtype=torch.float8_e4m3fn, device=U_.dev()), torch.empty(M, device=U_.dev())
+    G.gptq_quantize_e4m3(X, X8, xs)
+    a = np.max(np.abs(Xv), axis=1)
+    want = torch.from_numpy((448.0 * Xv / a[:, None]).astype(np.float32)).to(torch.float8_e4m3fn)
+    assert torch.equal(X8.cpu().float(), want.float())
+    assert np.all(np.abs(xs.double().cpu().numpy() - a / 448.0) <= 2.0 ** -24 * a / 448.0)
