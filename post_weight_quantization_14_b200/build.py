@@ -29,7 +29,7 @@ def nvcc_path() -> str:
 
 def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(PKG, "csrc", "*.cu")) + glob.glob(os.path.join(PKG, "csrc", "*.cuh"))
-                  + [os.path.join(ROOT, "include", "gptq_b200.h")])
+                  + glob.glob(os.path.join(PKG, "csrc", "*.h")) + [os.path.join(ROOT, "include", "gptq_b200.h")])
 
 
 def up_to_date() -> bool:

@@ -52,6 +52,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "host_once.h"
 #include "pack.cuh"
 
 namespace gq {
@@ -579,14 +580,15 @@ namespace gqh {
 // Tensor maps are encoded anew on every call: a shared cache would tie concurrent callers together.
 inline bool tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type, int elem_bytes, uint64_t rows,
                     uint64_t cols, uint32_t box_rows, uint32_t box_cols, bool swizzle) {
-    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    static KeepFound<PFN_cuTensorMapEncodeTiled_v12000> found;
+    const auto encode = found.get([] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
             q != cudaDriverEntryPointSuccess)
             fn = nullptr;
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }();
+    });
     if (!encode) return false;
     cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * (uint64_t)elem_bytes};
     cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
@@ -595,15 +597,22 @@ inline bool tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The setmaxnreg split relies on the registers that the kernel was launched with.
+// The setmaxnreg split relies on the registers that the kernel was launched with: with fewer it would wait
+// forever, so such a build is refused.
 template <auto Kernel>
-bool d8_registers_fit() {
-    static const bool fit = [] {
-        cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(Kernel)) == cudaSuccess &&
-               at.numRegs == gq::D8_REGS;
-    }();
-    return fit;
+cudaError_t d8_registers_fit() {
+    static KeepFound<int> found;
+    cudaError_t e = cudaSuccess;
+    const int regs = found.get([&e] {
+        cudaFuncAttributes at = {};
+        e = cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(Kernel));
+        return e == cudaSuccess ? at.numRegs : 0;
+    });
+    if (regs == 0) {
+        (void)cudaGetLastError();   // a failed query must not leak into later checks
+        return e;
+    }
+    return regs >= gq::D8_REGS ? cudaSuccess : cudaErrorInvalidKernelImage;
 }
 
 int num_sms();
@@ -617,7 +626,7 @@ cudaError_t dq_gemm_e4m3_launch(const uint8_t* X8, const int32_t* qweight, gq::D
                  (uint64_t)p.N, Cfg::KW, 128, false))
         return cudaErrorInvalidValue;
     constexpr auto kern = gq::dq_gemm_e4m3_kernel<BITS, TT>;
-    if (!d8_registers_fit<kern>()) return cudaErrorInvalidKernelImage;
+    GQ_TRY((d8_registers_fit<kern>()));
     GQ_TRY((smem_attr_once<kern, Cfg::SMEM>()));
     p.tiles_n = (p.N + 127) / 128;
     const long long tiles = (long long)p.tiles_n * ((p.M + TT - 1) / TT);
