@@ -422,7 +422,7 @@ bool make_tmap_2d_plain(CUtensorMap* map, const void* base, uint64_t rows, uint6
 // MaxDynamicSharedMemorySize of one kernel, set once per device; safe from several threads (setting
 // it twice changes nothing).
 template <auto Kernel, int BYTES>
-cudaError_t smem_attr_once() {
+static cudaError_t smem_attr_once() {
     static std::atomic<bool> done[128];
     int dev = 0;
     GQ_TRY(cudaGetDevice(&dev));

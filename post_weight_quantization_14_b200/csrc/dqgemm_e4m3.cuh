@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
 namespace gqh {
 
 // Tensor maps are encoded anew on every call: a shared cache would tie concurrent callers together.
-inline bool tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type, int elem_bytes, uint64_t rows,
+static bool tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type, int elem_bytes, uint64_t rows,
                     uint64_t cols, uint32_t box_rows, uint32_t box_cols, bool swizzle) {
     static KeepFound<PFN_cuTensorMapEncodeTiled_v12000> found;
     const auto encode = found.get([] {
@@ -600,7 +600,7 @@ inline bool tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type
 // The setmaxnreg split relies on the registers that the kernel was launched with: with fewer it would wait
 // forever, so such a build is refused.
 template <auto Kernel>
-cudaError_t d8_registers_fit() {
+static cudaError_t d8_registers_fit() {
     static KeepFound<int> found;
     cudaError_t e = cudaSuccess;
     const int regs = found.get([&e] {

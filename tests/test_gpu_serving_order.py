@@ -2,6 +2,8 @@
 producer in another stream, right behind a kernel of their own stream, eagerly and in a captured fork
 and join.  Before each call the inputs hold other values, so a call that starts early is seen."""
 
+import shutil
+
 import numpy as np
 import pytest
 import torch
@@ -9,7 +11,7 @@ import torch
 from post_weight_quantization_14_b200 import gptq as G
 
 from . import gpu_util as U_
-from .test_gpu_serving import Packed, _activations, _bf16, _e4m3
+from .test_gpu_serving import Packed, _activations, _bf16, _e4m3, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +112,32 @@ def test_behind_a_join_of_captured_streams(op):
         graph.replay()
         torch.cuda.synchronize()
         _same(b, y)
+
+
+def test_two_copies_of_the_library_in_one_process(tmp_path):
+    # what one copy has set up for its kernels says nothing about the other's
+    rng = np.random.default_rng(16)
+    L = Packed(rng, 136, 512, 4, 128, False)
+    A = Packed(rng, 136, 512, 4, 128, False, 1)
+    X, Xv, xs, xsv = _x(rng, 70, 512, "e4m3")
+    first = G.lib()
+    try:
+        for k in range(2):
+            Y, Z, V = (torch.empty((m, 136), device=U_.dev()) for m in (70, 9, 9))
+            L.gemm(X, xs, Y)
+            L.gemv(X[:9], Z, xs[:9])
+            A.gemv(X[:9], V, xs[:9])
+            G.gptq_sync_status()
+            L.check(Y, Xv, xsv)
+            L.check(Z, Xv[:9], xsv[:9])
+            A.check(V, Xv[:9], xsv[:9])
+            if k == 0:
+                copy = tmp_path / "libgptq_b200_copy.so"
+                shutil.copy(G.LIB_PATH, copy)
+                G._lib, path, G.LIB_PATH = None, G.LIB_PATH, str(copy)
+                try:
+                    assert G.lib() is not first
+                finally:
+                    G.LIB_PATH = path
+    finally:
+        G._lib = first
