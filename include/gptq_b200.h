@@ -302,8 +302,9 @@ gptq_status gptq_quantize_e4m3(const void* X, gptq_dtype xt, int64_t M, int64_t 
 
 /* Y[m, n] = x_scale[m] * sum_k X8[m, k] * W_hat[n, k] for any number of rows: gptq_dequant_gemm on
  * 8-bit activations.  X8 and x_scale as written by the two calls above, Y bf16 or fp32 (yt).
- * Codes and zero points of 2, 3 and 4 bits are exact in e4m3, and so are a group's products; they are
- * summed in fp32, scaled by the group's fp16 scales and summed in fp32 in a fixed order.
+ * q - z of 2, 3 and 4 bits is exact in e4m3, and so are a group's products with X8; they are summed in
+ * fp32, scaled by the group's fp16 scales and summed in fp32 in a fixed order.  A row of W_hat that is 0
+ * (every code at its zero point) gives exact zeros for finite X8 and x_scale.
  * Requires bits 2, 3 or 4, group_size -1 or 32, 64, 128 dividing d_in, desc_act 0
  * (GPTQ_ERR_UNSUPPORTED otherwise), d_in % 32 == 0, d_out % 8 == 0, X8, Y and the packed arrays
  * 16-byte aligned.  No workspace. */

@@ -2,7 +2,7 @@
 //
 //   Y[m, n] = xs[m] sum_g s_g[n] P_g[n, m],   P_g[n, m] = sum_{k in g} (q[n, k] - z_g[n]) X8[m, k]
 //
-// Codes and zero points of 2, 3 and 4 bits are exact in e4m3, so P_g is formed by the 8-bit tensor
+// q - z of 2, 3 and 4 bits is exact in e4m3, so P_g is formed by the 8-bit tensor
 // instructions (twice the bf16 rate) from exact products with fp32 accumulation; s_g and xs are
 // applied in fp32.  No rounded copy of W_hat is made.
 //
@@ -26,21 +26,19 @@
 // (GPTQ_ERR_TIMEOUT).  No TMA multicast.
 //
 // Codes to e4m3: a byte b < 16 read as e4m3 is b 2^-9 (the subnormals and the first binade are one
-// arithmetic sequence), so spreading the codes to bytes already gives q 2^-9, and 0x80 | z is -z 2^-9.
-// P_g 2^-9 = sum q 2^-9 X8 + sum (-z 2^-9) X8: the second sum takes the same MMAs again with an
-// operand of 32 equal columns.  That doubles the tensor work, which had three quarters of the time to
-// spare, and more than halves the converters' integer work: looking q - z up in registers by byte
-// permutes took 11 instructions for 8 codes against 5 (4096 x 4096 x 2048 tokens: 83 us against 78 us
-// when this was chosen).
+// arithmetic sequence), so |q - z|, with the sign in bit 7, is (q - z) 2^-9.  A group's 2^BITS bytes come
+// as 4 registers from a table of 16 zero points in shared memory, and byte permutes look four codes up.
+// The MMAs then sum exact products of q - z: P_g carries the rounding of sums of |q - z| |X8| and is 0
+// where every code is at the zero point.  (Spread codes as they are and a second pass of MMAs with -z
+// would round sums of (q + z) |X8|, which for codes near z can be hundreds of times larger.)
 //
-// What bounds it: each 128-column K tile takes about 900 clocks, of which the MMAs are 520 (eight of
-// 65 clocks) and an epilogue warp and a converter set are busy for most of it.  Neither leaving out the
-// code conversion (-4 %), the multiplications by s_g (-7 %) nor the second MMA pass (-10 %) changes it
-// much, nor a third converter set, nor a ring of six A operands with two accumulators: the roles'
-// latencies (a passed barrier is 100-200 clocks) are close to each other.  4-bit groups of 128:
-// 2048 tokens x 4096 x 4096 in 73 us (940 TFLOP/s), 8192 tokens x 11008 x 4096 in 650 us
-// (1140 TFLOP/s, 35 % of the 8-bit rate); groups of 32 take 174 us for the former, as every group is an
-// accumulator to drain.
+// What bounds it: no unit is full.  A 128-column K tile takes about 800 clocks, of which the MMAs are 260
+// (four of 65 clocks); converting one operand takes a set of four warps longer than that, two sets take
+// turns, and the epilogue's warps share the schedulers with them.  4-bit groups of 128, from a graph: 2048
+// tokens x 4096 x 4096 in 76 us (900 TFLOP/s), 8192 tokens x 11008 x 4096 in 663 us (1115 TFLOP/s, 34 % of
+// the 8-bit rate); groups of 64 and 32 take 104 and 169 us for the former, as every group is an accumulator
+// to drain.  Looking q - z up takes 11 instructions for 8 codes of 4 bits (3 or 2 bits: 3 after spreading
+// them to nibbles), spreading alone 5, which with the second pass of MMAs took 74 and 729 us.
 //
 // Few tiles: the K range is split over a cluster of S CTAs, whose partial sums are joined
 // through distributed shared memory in rank order.
@@ -65,6 +63,7 @@ constexpr int D8_AST = 3, D8_PST = 8, D8_LAG = 2;
 constexpr int D8_REGS = 96, D8_REGS_CONV = 56, D8_REGS_EPI = 160, D8_REGS_MISC = 48;
 static_assert(2 * D8_REGS_CONV + 2 * D8_REGS_EPI + D8_REGS_MISC <= D8_THREADS / 128 * D8_REGS, "register split");
 constexpr int D8_PAR_S = 1024, D8_PAR_Z = 256;   // bytes of scales and zero points of four groups
+constexpr int D8_LUT = 256;                      // bytes of (q - z) 2^-9 as e4m3 for 16 z, 16 q
 constexpr int D8_SEG_TILES = 4;   // K tiles per segment for one group per row: 16 MMAs in place
 
 template <int BITS, int TT>
@@ -76,18 +75,16 @@ struct D8Cfg {
     static constexpr int FIT = (206 * 1024) / STAGE_BYTES;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;
     static constexpr int C = TT / 2;                  // tokens per epilogue warp
-    static constexpr int ND = 384 / TT;               // accumulators, at most (see acc_cols)
+    static constexpr int ND = 384 / TT;               // accumulators
     static constexpr int SMEM =
-        1024 + STAGES * STAGE_BYTES + D8_PST * (D8_PAR_S + D8_PAR_Z) + 8 * TT + 512;
+        1024 + STAGES * STAGE_BYTES + D8_PST * (D8_PAR_S + D8_PAR_Z) + D8_LUT + 8 * TT + 512;
     static_assert(STAGE_BYTES % 1024 == 0, "the swizzled tiles stay 1024-byte aligned");
     static_assert(TT * 128 * 4 <= STAGES * STAGE_BYTES, "partial sums fit the ring");
 };
 
-// Tensor memory: accumulators in front, then a ring of D8_AST operands: 32 columns of codes and 8 for
-// each group's zero point.
-__host__ __device__ constexpr int d8_acc_cols(int spt) { return spt <= 1 ? 384 : 256; }
-__host__ __device__ constexpr int d8_a_cols(int spt) { return 32 + 8 * (spt > 1 ? spt : 1); }
-static_assert(d8_acc_cols(1) + D8_AST * d8_a_cols(1) <= 512 && d8_acc_cols(4) + D8_AST * d8_a_cols(4) <= 512, "TMEM");
+// Tensor memory: accumulators in front, then a ring of D8_AST operands of 32 columns.
+constexpr int D8_ACC_COLS = 384, D8_A_COLS = 32;
+static_assert(D8_ACC_COLS + D8_AST * D8_A_COLS <= 512, "TMEM");
 
 struct D8Args {
     const __half* scales;    // [n_groups, N]
@@ -135,21 +132,15 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// 32 lanes x 8 consecutive columns, one column per register.
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(s));
     return r;
 }
-// The 32 codes of BITS words as 8 words of one code per byte.
+// The 32 codes of BITS words as 8 words of one e4m3 byte per code, taken from t, whose byte q stands for
+// code q.
 template <int BITS>
-__device__ __forceinline__ void codes_to_bytes(const uint32_t (&w)[BITS], uint32_t* out) {
+__device__ __forceinline__ void codes_to_bytes(const uint32_t (&w)[BITS], const uint4& t, uint32_t* out) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint32_t v;   // eight codes, one per nibble
@@ -160,9 +151,15 @@ __device__ __forceinline__ void codes_to_bytes(const uint32_t (&w)[BITS], uint32
         else
             v = codes_to_nibbles<3>(
                 (c == 0 ? w[0] : c == 3 ? w[2] >> 8 : __funnelshift_r(w[c - 1], w[c], c == 1 ? 24 : 16)) & 0xFFFFFFu);
-        const uint32_t even = v & 0x0F0F0F0Fu, odd = (v >> 4) & 0x0F0F0F0Fu;
-        out[2 * c] = byte_perm(even, odd, 0x5140u);
-        out[2 * c + 1] = byte_perm(even, odd, 0x7362u);
+        // a selector takes four nibbles, of which bits 0-2 pick one of eight bytes and bit 3 must be 0
+        if constexpr (BITS == 4) {
+            const uint32_t low = v & 0x77777777u, high = ((v >> 1) & 0x44444444u) | 0x32103210u;
+            out[2 * c] = byte_perm(byte_perm(t.x, t.y, low), byte_perm(t.z, t.w, low), high);
+            out[2 * c + 1] = byte_perm(byte_perm(t.x, t.y, low >> 16), byte_perm(t.z, t.w, low >> 16), high >> 16);
+        } else {
+            out[2 * c] = byte_perm(t.x, t.y, v);
+            out[2 * c + 1] = byte_perm(t.x, t.y, v >> 16);
+        }
     }
 }
 
@@ -205,8 +202,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset, so that accesses stay shared-memory ones
     uint8_t* par = smem + STAGES * Cfg::STAGE_BYTES;   // [PST] scales [4][128] fp16, zero points [4][16] words
+    uint8_t* lut = par + D8_PST * (D8_PAR_S + D8_PAR_Z);   // [16 zero points][16 codes]
     // [2][TT] scales of the tokens of this tile and the next
-    float* xs = reinterpret_cast<float*>(par + D8_PST * (D8_PAR_S + D8_PAR_Z));
+    float* xs = reinterpret_cast<float*>(lut + D8_LUT);
     uint64_t* full = reinterpret_cast<uint64_t*>(xs + 2 * TT);   // [STAGES] TMA landed
     uint64_t* empty = full + STAGES;                         // [STAGES] MMAs of the stage done
     uint64_t* conv = empty + STAGES;                         // [AST] A operand written
@@ -237,6 +235,10 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
         }
         fence_mbar_init();
     }
+    if (threadIdx.x < D8_LUT) {
+        const int d = (int)(threadIdx.x & 15) - (int)(threadIdx.x >> 4);
+        lut[threadIdx.x] = (uint8_t)(d < 0 ? 0x80 | -d : d);
+    }
     if (warp == 0) {
         __syncwarp();
         tmem_alloc(tmem_slot, 512);
@@ -246,10 +248,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();
-
-    const uint32_t a_ring = tmem + d8_acc_cols(p.spt), a_cols = d8_a_cols(p.spt);
-    const uint32_t nd = d8_acc_cols(p.spt) / TT;   // accumulators in use
+    const uint32_t a_ring = tmem + D8_ACC_COLS;
 
     // K tiles of this CTA, and the segments in them
     const int rank = p.split > 1 ? (int)cluster_rank() : 0;
@@ -267,16 +266,16 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
         const int qd = warp & 3, t = 32 * qd + lane;
         const uint32_t set = warp >> 2;
         const uint32_t a_row = a_ring + ((uint32_t)(32 * qd) << 16);
-        // units of four groups in a tile, and where the zero points of an operand's columns go stale:
-        // with every K tile, with every tile (one group per row) or never (no zero points given)
+        // units of four groups in a tile; one without groups in it (one group per row) is a single unit
         const uint32_t units = p.spt ? (nseg + 3) / 4 : 1;
+        const uint4* table = reinterpret_cast<const uint4*>(lut);
+        uint4 lookup = table[1 << (BITS - 1)];
         uint32_t it0 = 0, unit0 = 0, seen = ~0u;   // of the tile; last unit waited for
         bool ok = true;
         for (int w = first; w < p.tiles && ok; w += step, it0 += nkt, unit0 += units) {
             for (int kt = (int)((it0 ^ set) & 1); kt < nkt; kt += 2) {
                 const uint32_t it = it0 + kt, s = it % STAGES, a = it % D8_AST;
                 const int grp = kt * p.spt;   // the K tile's first group, counted from the CTA's first
-                const bool write_z = p.qzeros == nullptr ? it < D8_AST : p.spt || kt < D8_AST;
                 const uint32_t unit = unit0 + (uint32_t)grp / 4;
                 const bool fresh = p.qzeros != nullptr && unit != seen;
                 ok = warp_wait(w, &full[s], (it / STAGES) & 1, true, &aempty[a], ((it / D8_AST) & 1) ^ 1, true,
@@ -286,32 +285,28 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                 tc_fence_after();
                 const uint32_t* col =
                     reinterpret_cast<const uint32_t*>(smem + s * Cfg::STAGE_BYTES + Cfg::X_BYTES) + t;
-                const uint32_t dst = a_row + a_cols * a;
+                const uint32_t dst = a_row + D8_A_COLS * a;
+                const uint8_t* zq = par + (unit % D8_PST) * (D8_PAR_S + D8_PAR_Z) + D8_PAR_S;
+                auto zero_point = [&](int q) {   // of a group, counted as grp is
+                    const uint32_t* zw = reinterpret_cast<const uint32_t*>(zq + 64 * (q & 3));
+                    const int b = t * BITS;
+                    uint32_t z = zw[b >> 5] >> (b & 31);
+                    if (BITS == 3 && (b & 31) > 29) z |= zw[(b >> 5) + 1] << (32 - (b & 31));
+                    return z & ((1u << BITS) - 1u);
+                };
                 uint32_t words[4][BITS];
 #pragma unroll
                 for (int i = 0; i < 4 * BITS; ++i) words[i / BITS][i % BITS] = col[i * 128];
+                if (p.qzeros != nullptr && p.spt <= 1) lookup = table[zero_point(grp)];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t r[16];
-                    codes_to_bytes<BITS>(words[2 * h], r);
-                    codes_to_bytes<BITS>(words[2 * h + 1], r + 8);
+                    // groups of 64 and 32: the table changes within the K tile
+                    if (p.qzeros != nullptr && p.spt > 1) lookup = table[zero_point(grp + (p.spt >> 1) * h)];
+                    codes_to_bytes<BITS>(words[2 * h], lookup, r);
+                    if (p.qzeros != nullptr && p.spt > 2) lookup = table[zero_point(grp + 2 * h + 1)];
+                    codes_to_bytes<BITS>(words[2 * h + 1], lookup, r + 8);
                     tmem_st_32x32b_x16(dst + 16 * h, r);
-                }
-                if (write_z) {
-                    const uint8_t* zq = par + (unit % D8_PST) * (D8_PAR_S + D8_PAR_Z) + D8_PAR_S;
-                    for (int q = 0; q < (p.spt ? p.spt : 1); ++q) {   // each group's zero point, -z 2^-9
-                        uint32_t z = 1u << (BITS - 1);
-                        if (p.qzeros != nullptr) {
-                            const uint32_t* zw = reinterpret_cast<const uint32_t*>(zq + 64 * ((grp + q) & 3));
-                            const int b = t * BITS;
-                            z = zw[b >> 5] >> (b & 31);
-                            if (BITS == 3 && (b & 31) > 29) z |= zw[(b >> 5) + 1] << (32 - (b & 31));
-                            z &= (1u << BITS) - 1u;
-                        }
-                        z = (0x80u | z) * 0x01010101u;
-                        const uint32_t r[8] = {z, z, z, z, z, z, z, z};
-                        tmem_st_32x32b_x8(dst + 32 + 8 * q, r);
-                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -382,7 +377,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&dempty[buf]);
                 __syncwarp();
-                if (++buf == nd) {
+                if (++buf == ND) {
                     buf = 0;
                     dph ^= 1;
                 }
@@ -507,7 +502,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
         auto issue = [&](auto mm, uint32_t s, uint32_t a, int segs, bool open, bool close, int w) {
             constexpr int MM = decltype(mm)::value;
             const uint64_t xdesc = desc_sw128_kmajor(smem_u32(smem + s * Cfg::STAGE_BYTES));
-            const uint32_t at = a_ring + a_cols * a;
+            const uint32_t at = a_ring + D8_A_COLS * a;
 #pragma unroll
             for (int sg = 0; sg < 4 / MM; ++sg) {
                 if (sg >= segs) break;
@@ -523,16 +518,13 @@ __global__ void __launch_bounds__(D8_THREADS, 1)
                     for (int j = 0; j < MM; ++j)
                         umma_e4m3_ta(d, at + 8 * (sg * MM + j), xdesc + (uint64_t)(2 * (sg * MM + j)), idesc,
                                      j > 0 ? 1u : open ? 0u : 1u);
-#pragma unroll
-                    for (int j = 0; j < MM; ++j)
-                        umma_e4m3_ta(d, at + 32 + 8 * sg, xdesc + (uint64_t)(2 * (sg * MM + j)), idesc, 1u);
                     if (close) umma_commit(&dfull[buf]);
                 }
                 if (lead && sg == segs - 1) {
                     umma_commit(&empty[s]);
                     umma_commit(&aempty[a]);
                 }
-                if (close && ++buf == nd) {
+                if (close && ++buf == ND) {
                     buf = 0;
                     dph ^= 1;
                 }

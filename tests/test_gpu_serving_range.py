@@ -7,10 +7,11 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import gptq_oracle as O
 from post_weight_quantization_14_b200 import gptq as G
 
 from . import gpu_util as U_
-from .test_gpu_serving import _activations, _check_rows, _rows_reference, _tensor
+from .test_gpu_serving import Packed, _activations, _check_rows, _rows_reference, _tensor, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +89,69 @@ def test_quantize_boundaries_between_codes_at_any_magnitude(M, d, exp):
     want = torch.from_numpy((448.0 * Xv / a[:, None]).astype(np.float32)).to(torch.float8_e4m3fn)
     assert torch.equal(X8.cpu().float(), want.float())
     assert np.all(np.abs(xs.double().cpu().numpy() - a / 448.0) <= 2.0 ** -24 * a / 448.0)
+
+
+# ------------------------------------------------------------------------------------ e4m3 product
+
+def _near_zero_point(rng, d_out, d_in, bits, g, sym):
+    """A layer whose codes lie at the zero point but for one in twenty, a step away; every third row and
+    every second group of the rows after it lie at it altogether.  Zero points at both ends of the codes."""
+    L = Packed(rng, d_out, d_in, bits, g, sym)
+    top = (1 << bits) - 1
+    gi = np.arange(d_in) // (d_in if g == -1 else g)
+    z = np.full((L.ng, d_out), 1 << (bits - 1)) if sym else rng.choice([0, top, top - 1, top // 2], size=(L.ng, d_out))
+    step = rng.choice([-1, 1], size=(d_out, d_in)) * (rng.random((d_out, d_in)) < 0.05)
+    step[::3] = 0
+    step[1::3, gi % 2 == 0] = 0
+    codes = np.clip(z.T[:, gi] + step, 0, top)
+    sc = rng.uniform(0.5, 1.5, size=(L.ng, d_out)).astype(np.float16)
+    qw, qz = O.pack_qweight(codes, bits), None if sym else O.pack_qzeros(z, bits)
+    L.qw, L.qz, L.sc = U_.t(qw), None if sym else U_.t(qz), U_.t(sc)
+    L.What = O.dequant_packed(qw, sc, qz, d_out, d_in, bits, g, sym, None)
+    return L
+
+
+@pytest.mark.parametrize("M,d_out,d_in,bits,g,sym", [
+    (3, 264, 128, 4, 128, False), (70, 264, 128, 4, -1, False), (130, 136, 128, 4, 32, False), (40, 136, 128, 3, 64, False),
+    (200, 264, 128, 2, 128, False), (65, 136, 128, 4, 64, True), (2000, 1288, 128, 4, 128, False), (33, 136, 512, 4, -1, False),
+    (300, 264, 1024, 4, 128, False), (20, 136, 1024, 3, 32, True), (64, 264, 4096, 4, 128, False)])
+def test_gemm_e4m3_with_codes_at_the_zero_point(M, d_out, d_in, bits, g, sym):
+    # q - z and its products are exact, so a row with q = z is 0 exactly, and the others are off by at most
+    # one rounding, 2^-23 of S_g = sum |x| s |q - z|, for every 8 columns of a group or of a segment of 512
+    # (one group per row), and 2^-23 of S for every group or segment and each of up to 8 joins, the scale
+    # and the token's factor.
+    rng = np.random.default_rng(M + d_in + bits + g)
+    L = _near_zero_point(rng, d_out, d_in, bits, g, sym)
+    X, Xv, xs, xsv = _x(rng, M, d_in, "e4m3")
+    X = X.float().abs().to(torch.float8_e4m3fn)          # behind a gate: one sign
+    Xv = np.abs(Xv)
+    Y = torch.empty((M, d_out), device=U_.dev())
+    L.gemm(X, xs, Y)
+    G.gptq_sync_status()
+    got = Y.double().cpu().numpy()
+    dead = np.all(L.What == 0, axis=1)
+    assert dead.sum() >= d_out // 3
+    assert np.all(got[:, dead] == 0)
+    run = min(d_in, 512 if g == -1 else g)
+    S = (Xv @ np.abs(L.What).T) * xsv[:, None]
+    tol = (run / 8 + d_in / run + 10) * 2.0 ** -23 * S
+    err = np.abs(got - Xv @ L.What.T * xsv[:, None])
+    assert np.all(err <= tol), float(np.max(err / np.maximum(tol, 1e-300)))
+
+
+@pytest.mark.parametrize("bits,g,sym", [(4, 128, False), (4, 32, False), (3, 64, False), (2, -1, False), (4, 64, True)])
+def test_gemm_e4m3_extreme_codes_and_scales(bits, g, sym):
+    rng = np.random.default_rng(bits + g)
+    M, d_out, d_in = 37, 136, 256
+    L = Packed(rng, d_out, d_in, bits, g, sym)
+    top = (1 << bits) - 1
+    qw = O.pack_qweight(rng.choice([0, top], size=(d_out, d_in)), bits)
+    qz = None if sym else O.pack_qzeros(rng.choice([0, top], size=(L.ng, d_out)), bits)
+    sc = rng.choice([0.0, 2.0 ** -24, 6e-8, 65504.0, 1.0], size=(L.ng, d_out)).astype(np.float16)
+    L.qw, L.qz, L.sc = U_.t(qw), None if sym else U_.t(qz), U_.t(sc)
+    L.What = O.dequant_packed(qw, sc, qz, d_out, d_in, bits, g, sym, None)
+    X, Xv, xs, xsv = _x(rng, M, d_in, "e4m3")
+    Y = torch.empty((M, d_out), device=U_.dev())
+    L.gemm(X, xs, Y)
+    G.gptq_sync_status()
+    L.check(Y, Xv, xsv)
