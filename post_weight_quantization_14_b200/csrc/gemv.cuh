@@ -491,9 +491,9 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
                         mma_16816(part[j][mt], a[2], b[2], a[3], b[3], xb[mt][2], xb[mt][3], XT());
                     }
                 }
-                if (GROUPS == 1 ? p.gshift == 7 && (s4 == 3 || k + 32 >= K)
-                                : ((k + 32) & gmask) == 0 || k + 32 >= K)
-                    flush();
+                // one group per row as well: the tensor instruction may cut its sums off, always in the same
+                // direction, so they are added up in fp32 every 128 columns
+                if (GROUPS == 1 ? s4 == 3 || k + 32 >= K : ((k + 32) & gmask) == 0 || k + 32 >= K) flush();
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -522,7 +522,6 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
     }
-    if (p.gshift > 7) flush();   // one group per row
 
     // ---- join the two runs of columns, then the CTAs of the cluster, in a fixed order
     __syncthreads();
@@ -697,7 +696,32 @@ __global__ void __launch_bounds__(GA_THREADS, MT == 1 ? 3 : 2) gemv_act_kernel(c
         for (int mt = 0; mt < MT; ++mt)
             if (m0 + 8 * mt + gid < p.M) q.x[mt] = load_x8(X + (long long)(m0 + 8 * mt + gid) * K + k);
     };
-    float sum[2][MT][4] = {};   // tile j: rows n0 + j and n0 + j + 2
+    // Tile j: rows n0 + j and n0 + j + 2.  The tensor instruction may cut its sums off, always in the same
+    // direction, so those of 32 columns are added up in fp32.  Four token tiles leave no registers for that
+    // (64 tokens through 4096 x 11008: 117 us) and add those of 64 columns to sums in shared memory (106 us).
+    constexpr bool PARKED = MT == 4;
+    float sum[2][MT][4] = {}, part[2][MT][4] = {};
+    float4* parked = reinterpret_cast<float4*>(ga_smem + (TABLE ? p.ng * ROWS * 4 : 0)) + warp * (2 * MT * 32) + lane;
+    bool odd = false;
+    auto add_part = [&] {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (PARKED) {
+                    float4& s = parked[(j * MT + mt) * 32];
+                    const float4 v = s;
+                    s = make_float4(v.x + part[j][mt][0], v.y + part[j][mt][1], v.z + part[j][mt][2], v.w + part[j][mt][3]);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (!PARKED) sum[j][mt][c] += part[j][mt][c];
+                    part[j][mt][c] = 0.f;
+                }
+            }
+    };
+    if (PARKED)
+        for (int i = 0; i < 2 * MT; ++i) parked[i * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
     Chunk now = {}, next = {};
     int st = s0 + warp;
     if (st < s1) load(st, now);
@@ -752,10 +776,23 @@ __global__ void __launch_bounds__(GA_THREADS, MT == 1 ? 3 : 2) gemv_act_kernel(c
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        mma_16816(sum[j][mt], a[c][j][0], a[c][j + 2][0], a[c][j][1], a[c][j + 2][1], xb[mt][2 * h],
+                        mma_16816(part[j][mt], a[c][j][0], a[c][j + 2][0], a[c][j][1], a[c][j + 2][1], xb[mt][2 * h],
                                   xb[mt][2 * h + 1], __nv_bfloat16());
         }
+        if (!PARKED || odd) add_part();
+        odd = !odd;
         now = next;
+    }
+    if (PARKED) {
+        add_part();
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const float4 v = parked[i * 32];
+            sum[i / MT][i % MT][0] = v.x;
+            sum[i / MT][i % MT][1] = v.y;
+            sum[i / MT][i % MT][2] = v.z;
+            sum[i / MT][i % MT][3] = v.w;
+        }
     }
 
     __syncthreads();
@@ -841,7 +878,9 @@ template <int BITS, typename XT, int MT, bool TABLE>
 cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
     constexpr int TOK = 8 * MT, ROWS = gq::GA_ROWS;
     constexpr auto kern = gq::gemv_act_kernel<BITS, XT, MT, TABLE>;
-    GQ_TRY((smem_attr_once<kern, gq::GA_TABLE>()));
+    constexpr int SUMS = gq::GA_THREADS / 32 * TOK * ROWS * 4;   // of the warps, in the table's place when it is done with
+    constexpr int PARKED = MT == 4 ? SUMS : 0;
+    GQ_TRY((smem_attr_once<kern, gq::GA_TABLE + PARKED>()));
     p.nblocks = (unsigned)((p.N + ROWS - 1) / ROWS);
     p.vec = p.N % 4 == 0;
     const long long blocks = (long long)p.nblocks * ((p.M + TOK - 1) / TOK);
@@ -853,7 +892,7 @@ cudaError_t gemv_act_launch(gq::GemvArgs p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks * p.split));
     cfg.blockDim = dim3(gq::GA_THREADS);
-    cfg.dynamicSmemBytes = std::max(TABLE ? (size_t)p.ng * ROWS * 4 : 0, (size_t)(gq::GA_THREADS / 32) * TOK * ROWS * 4);
+    cfg.dynamicSmemBytes = std::max((TABLE ? (size_t)p.ng * ROWS * 4 : 0) + PARKED, (size_t)SUMS);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -11,7 +11,7 @@ from oracle import gptq_oracle as O
 from post_weight_quantization_14_b200 import gptq as G
 
 from . import gpu_util as U_
-from .test_gpu_serving import Packed, _activations, _check_rows, _rows_reference, _tensor, _x
+from .test_gpu_serving import Packed, _activations, _bf16, _check_rows, _e4m3, _rows_reference, _tensor, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -155,3 +155,50 @@ def test_gemm_e4m3_extreme_codes_and_scales(bits, g, sym):
     L.gemm(X, xs, Y)
     G.gptq_sync_status()
     L.check(Y, Xv, xsv)
+
+
+# ------------------------------------------------------------------------------------ long rows of one sign
+
+def _tiled(rng, d_out, d_in, bits, g, act):
+    """A layer of 32 different rows, over and over (enough blocks of rows that K is not split), with
+    positive weights: every rounding of a sum in one direction would add up."""
+    L = Packed(rng, 32, d_in, bits, g, False, act)
+    top = (1 << bits) - 1
+    qw = O.pack_qweight(rng.integers(1, top + 1, size=(32, d_in)), bits)
+    qz = O.pack_qzeros(np.zeros((L.ng, 32), dtype=np.int64), bits)
+    sc = rng.uniform(0.5, 1.5, size=(L.ng, 32)).astype(np.float16)
+    L.What = O.dequant_packed(qw, sc, qz, 32, d_in, bits, g, False, None if L.gi is None else L.gi.cpu().numpy())
+    rep = d_out // 32
+    L.qw, L.sc = U_.t(qw).repeat(1, rep).contiguous(), U_.t(sc).repeat(1, rep).contiguous()
+    L.qz = U_.t(qz).repeat(1, rep).contiguous()          # 32 codes fill whole words
+    L.args = (d_out, d_in, bits, g, False)
+    return L
+
+
+@pytest.mark.parametrize("M,d_out,bits,g,act,x", [
+    (3, 56832, 2, -1, 0, "bf16"), (3, 56832, 2, -1, 0, "e4m3"), (3, 9472, 4, 128, 1, "bf16"), (3, 9472, 2, 64, 1, "e4m3"),
+    (3, 9472, 3, 16, 1, "bf16"), (12, 9472, 4, 128, 1, "bf16"), (50, 9472, 4, 64, 1, "bf16"), (33, 9472, 2, 64, 1, "e4m3")])
+def test_gemv_of_long_rows_has_no_bias(M, d_out, bits, g, act, x):
+    # A tensor instruction may cut its sums off: at most 2^-23 of a partial sum each time, always in the same
+    # direction.  As a partial sum takes 8 of them at most before it is added to the total in fp32 (rounded
+    # to nearest), that is 8 2^-23 of the sum.  A warp adds some 256 partial sums, whose roundings to nearest
+    # are independent: 2^-24 of the sum each, taken as if at its end throughout; five standard deviations
+    # (each 2^-24 / sqrt 3) are allowed, and four roundings for joins, scales and the token's factor.
+    rng = np.random.default_rng(bits + g + d_out)
+    d_in = 65536
+    L = _tiled(rng, d_out, d_in, bits, g, act)
+    a = np.abs(_activations(rng, M, d_in))   # of many magnitudes, so that sums have bits to lose
+    xs = xsv = None
+    if x == "bf16":
+        X, Xv = _bf16(a)
+    else:
+        X, Xv = _e4m3(a * 20)
+        xsv = np.full(M, 0.5)
+        xs = U_.t(xsv.astype(np.float32))
+    Y = torch.empty((M, d_out), device=U_.dev())
+    L.gemv(X, Y, xs)
+    G.gptq_sync_status()
+    ref = Xv @ L.What.T * (1.0 if xsv is None else xsv[:, None])
+    rel = Y.double().cpu().numpy().reshape(M, d_out // 32, 32) / ref[:, None, :] - 1
+    tol = 8 * 2.0 ** -23 + (5 * np.sqrt(256 / 3) + 4) * 2.0 ** -24
+    assert np.all(np.abs(rel) <= tol), (float(np.abs(rel).max() / tol), float(rel.mean() / tol))
