@@ -233,8 +233,10 @@ constexpr int GM_WSTRIDE = 4 * GM_ROWS + 32;
 template <int BITS, typename XT, int MT, int GROUPS>
 struct GmCfg {
     // CTAs of an SM, as registers go: 3 against 2 for up to eight tokens took the 50001 x 8192 product
-    // above from 123 to 101 us
-    static constexpr int CTAS = MT == 4 || GROUPS == 8 ? 1 : MT == 1 && GROUPS == 1 && BITS <= 4 ? 3 : 2;
+    // above from 123 to 101 us.  Two token tiles with groups of 32 or 64 do not fit the 96 registers of two
+    // CTAs: 16 tokens through 11008 x 4096, groups of 64, take 32 us with one and 36 us with two (3 bits),
+    // 28 and 31 us (4 bits); only 2 bits with e4m3 tokens go the other way (32 and 28 us).
+    static constexpr int CTAS = MT == 4 || GROUPS == 8 || (MT == 2 && GROUPS == 4) ? 1 : MT == 1 && GROUPS == 1 && BITS <= 4 ? 3 : 2;
     static constexpr int TOK = 8 * MT;
     static constexpr int WROWS = GM_K * BITS / 32;
     static constexpr int W_BOX = WROWS * 128;   // 32 rows n by TMA
