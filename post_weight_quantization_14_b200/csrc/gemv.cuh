@@ -279,7 +279,6 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
         fence_mbar_init();
     }
     __syncthreads();
-    pdl_wait();
 
     // Without TMA (N no multiple of 4, or e4m3 rows that are no multiple of 16 bytes) rows that start
     // between two 16-byte boundaries are copied from the boundary on, and the reader skips the 'skew'.
