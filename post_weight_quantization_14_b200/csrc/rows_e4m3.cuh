@@ -10,7 +10,7 @@
 // whose order is that of the magnitudes with NaN above infinity, so a NaN reaches x_scale.
 //
 // Bound by memory for many rows: 2048 x 4096 bf16 with residual 12 us (58.7 MB, 4.9 TB/s; of it about
-// 2.5 us launch and tail), 8192 rows 37.6 us (6.2 TB/s), 4096 x 11008 bf16 without norm 28 us (4.8 TB/s),
+// 2.5 us launch and tail), 8192 rows 37.6 us (6.2 TB/s), 4096 x 11008 bf16 without norm 24 us (5.7 TB/s),
 // 8191 x 16384 fp32 122 us (5.5 TB/s); by latency for few: 2.4 us for one row, 2.7 us for 64.  Long rows
 // (512 x 65536 bf16 with residual) take 63 us; without the code for sums that fp32 does not hold, 57 us.
 #pragma once
@@ -242,6 +242,16 @@ __global__ void __launch_bounds__(rw_max_threads(VEC), VEC == 1 && sizeof(XT) + 
     SquareSum kept;   // KEEP
     float sum = 0.f;
     uint32_t top = 0;
+    // With a norm apart from the sums above, so that w may come last (4096 x 8192 bf16, fp32 w: 25 us against
+    // 30 us); without one at once, for its registers (4096 x 11008 bf16: 24 us against 35 us).
+    auto weigh = [&](float(&h)[8], const Raw8<WT>& w) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (NORM && !KEEP) sum = fmaf(h[j], h[j], sum);
+            if (NORM) h[j] *= w.at(j);
+            top = max(top, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+        }
+    };
     constexpr int FLIGHT = VEC > 4 ? 4 : VEC;   // vectors of each input in flight
 #pragma unroll
     for (int i0 = 0; i0 < VEC; i0 += FLIGHT) {
@@ -268,17 +278,12 @@ __global__ void __launch_bounds__(rw_max_threads(VEC), VEC == 1 && sizeof(XT) + 
                 for (int j = 0; j < 8; ++j) h[j] += r[i].at(j);
                 if (c0 + (i0 + i) * step < D) store8(reinterpret_cast<XT*>(p.R2) + row * p.D + c0 + (i0 + i) * step, h);
             }
+            if (!NORM) weigh(h, w[i]);
         }
-        if (NORM && KEEP) kept.add<FLIGHT>(v + i0);
+        if (KEEP) kept.add<FLIGHT>(v + i0);
+        if (NORM) {
 #pragma unroll
-        for (int i = 0; i < FLIGHT; ++i) {
-            float(&h)[8] = v[i0 + i];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (NORM && !KEEP) sum = fmaf(h[j], h[j], sum);
-                if (NORM) h[j] *= w[i].at(j);
-                top = max(top, __float_as_uint(h[j]) & 0x7FFFFFFFu);
-            }
+            for (int i = 0; i < FLIGHT; ++i) weigh(v[i0 + i], w[i]);
         }
     }
     if (KEEP) sum = kept.far == 0.f ? kept.mid : __int_as_float(0x7F800000);   // infinity: not held
@@ -383,8 +388,8 @@ cudaError_t rows_e4m3_run(gq::RowsArgs p, long long M, const char* name, cudaStr
     if (vecs > gq::RW_MAX_VECS)
         return launch_plain(gq::rows_e4m3_long_kernel<XT, WT, NORM>, grid, dim3(1024), 0, st, p);
     // Few rows: a vector a thread, for latency.  Many rows: four, for bytes in flight and cheap barriers;
-    // eight for long rows without R, whose registers they leave enough of (4096 x 11008 bf16: 28 us against
-    // 32 us with four; with R they do not: 2048 x 11008 took 37 us against 29 us).
+    // eight for long rows without R, whose registers they leave enough of (4096 x 11008 bf16: 24 us, with four
+    // 28 us; 8191 x 16384 fp32 norm: 122 and 163 us).  With R they do not (2048 x 11008: 39 us, with four 30 us).
     const bool few = M <= 2 * num_sms();
     int vec = few ? 1 : p.R == nullptr && vecs > 512 ? 8 : 4, threads;
     while (vec * gq::rw_max_threads(vec) < vecs) vec *= 2;
