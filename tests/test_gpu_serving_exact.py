@@ -62,6 +62,7 @@ GEMV = [
     # activation order, the table in shared memory
     (64, 70, 16384, 4, 16, False, 1, "bf16"),
     (12, 45, 65536, 4, 128, False, 1, "e4m3"),
+    (64, 33, 20480, 4, 16, False, 1, "e4m3"),     # 1280 groups: the largest table, beside the sums of 32 tokens
     (33, 45, 20488, 2, 128, False, 1, "bf16"),
     (1, 36, 65536, 3, 64, False, 2, "bf16"),
     (5, 39, 32760, 8, 32, False, 1, "e4m3"),
