@@ -271,9 +271,10 @@ gptq_status gptq_dequant_gemm(const void* X, int64_t M, const int32_t* qweight, 
  *            [0, n_groups) is reported by the next gptq_sync_status() (GPTQ_ERR_INVALID_ARG).
  *   Y        device [M, d_out] row-major, bf16 or fp32 (yt), written in full; apart from the inputs.
  * Sums are fp32 in a fixed order (the same bits on every run); no rounded copy of W_hat is made,
- * and a bf16 Y is rounded once.  A non-finite X makes its own row of Y non-finite and no other.
- * Requires 1 <= M <= GPTQ_GEMV_MAX_M, d_in % 8 == 0, 1 <= d_out; X, qweight, scales and qzeros
- * 16-byte aligned.  No workspace, nothing is allocated. */
+ * and a bf16 Y is rounded once.  A non-finite X makes its own row of Y non-finite and no other, and
+ * so does a finite one whose sums of |X (q - z)| over 128 columns leave the range of fp32.
+ * Requires 1 <= M <= GPTQ_GEMV_MAX_M, d_in % 8 == 0, d_in <= 65536, 1 <= d_out <= 2^30; X, qweight,
+ * scales and qzeros 16-byte aligned.  No workspace, nothing is allocated. */
 #define GPTQ_GEMV_MAX_M 64
 gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale, int64_t M, const int32_t* qweight,
                               const uint16_t* scales, const int32_t* qzeros, const int32_t* g_idx, int64_t d_out,
@@ -282,7 +283,8 @@ gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale
 /* ------------------------------------------------------------------ 8-bit activations
  * gptq_rms_norm_e4m3, for each of the M rows:
  *   h = X + residual (X alone without one),  y_k = h_k weight_k / sqrt(mean_k h_k^2 + eps),
- *   x_scale = max_k |y_k| / 448,  X8_k = e4m3(y_k / x_scale) (nearest, ties to even),
+ *   x_scale = max_k |y_k| / 448,  X8_k = e4m3(448 y_k / max_k |y_k|) (nearest, ties to even; the
+ *   quotient is taken to 48 bits, not from the rounded x_scale),
  *   residual_out = h rounded to X's type.
  * gptq_quantize_e4m3 does the same for y = X.
  *   X, residual, residual_out  device [M, d_in] row-major, bf16 or fp32 (xt).  residual and
@@ -293,6 +295,8 @@ gptq_status gptq_dequant_gemv(const void* X, gptq_dtype xt, const float* x_scale
  * gets x_scale 0 and zero codes.  A row with a NaN or an infinity gets a non-finite x_scale (its
  * products are then non-finite) and leaves the others alone.  Finite rows of any magnitude and any
  * eps >= 0, as far as h and h weight are neither infinite nor subnormal in fp32.
+ * x_scale is rounded to fp32: below 2^-126 (rows of y below 2^-117) it keeps fewer bits, below 2^-150
+ * it is 0.
  * Requires d_in % 8 == 0, d_in <= 65536; X8 8-byte, the other arrays 16-byte aligned (x_scale 4). */
 gptq_status gptq_rms_norm_e4m3(const void* X, const void* residual, gptq_dtype xt, const void* weight, gptq_dtype wt,
                                int64_t M, int64_t d_in, float eps, uint8_t* X8, float* x_scale, void* residual_out,
@@ -306,8 +310,10 @@ gptq_status gptq_quantize_e4m3(const void* X, gptq_dtype xt, int64_t M, int64_t 
  * fp32, scaled by the group's fp16 scales and summed in fp32 in a fixed order.  A row of W_hat that is 0
  * (every code at its zero point) gives exact zeros for finite X8 and x_scale.
  * Requires bits 2, 3 or 4, group_size -1 or 32, 64, 128 dividing d_in, desc_act 0
- * (GPTQ_ERR_UNSUPPORTED otherwise), d_in % 32 == 0, d_out % 8 == 0, X8, Y and the packed arrays
- * 16-byte aligned.  No workspace. */
+ * (GPTQ_ERR_UNSUPPORTED otherwise), d_in % 32 == 0, d_in <= 65536, d_out % 8 == 0, M and d_out at most
+ * 2^30 - 256, X8, Y and the packed arrays 16-byte aligned.  No workspace.  A layer in activation order, with
+ * 8 bits, groups of 16 or an odd d_out has no such form: gptq_dequant_gemv takes its tokens in runs of
+ * GPTQ_GEMV_MAX_M. */
 gptq_status gptq_dequant_gemm_e4m3(const uint8_t* X8, const float* x_scale, int64_t M, const int32_t* qweight,
                                    const uint16_t* scales, const int32_t* qzeros, int64_t d_out, int64_t d_in,
                                    const gptq_config* cfg, void* Y, gptq_dtype yt, void* stream);

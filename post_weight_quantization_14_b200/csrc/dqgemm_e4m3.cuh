@@ -32,9 +32,9 @@
 // where every code is at the zero point.  (Spread codes as they are and a second pass of MMAs with -z
 // would round sums of (q + z) |X8|, which for codes near z can be hundreds of times larger.)
 //
-// What bounds it: no unit is full.  A 128-column K tile takes about 800 clocks, of which the MMAs are 260
-// (four of 65 clocks); converting one operand takes a set of four warps longer than that, two sets take
-// turns, and the epilogue's warps share the schedulers with them.  4-bit groups of 128, from a graph: 2048
+// What bounds it: no unit is full.  A 128-column K tile takes about 1070 clocks (2048 tokens x 4096 x 4096),
+// of which the MMAs are 260 (four of 65 clocks); 66 % of the issue slots are used, most by the converters and
+// the epilogue, whose latencies add up along the ring of operands.  4-bit groups of 128: 2048
 // tokens x 4096 x 4096 in 76 us (900 TFLOP/s), 8192 tokens x 11008 x 4096 in 663 us (1115 TFLOP/s, 34 % of
 // the 8-bit rate); groups of 64 and 32 take 104 and 169 us for the former, as every group is an accumulator
 // to drain.  Looking q - z up takes 11 instructions for 8 codes of 4 bits (3 or 2 bits: 3 after spreading

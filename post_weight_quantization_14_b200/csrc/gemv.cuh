@@ -9,25 +9,29 @@
 //
 // gemv_mma_kernel (groups of consecutive columns).  The work is one pass over the packed words, so
 // the design is about issue slots next to the loads: with fp32 FMAs every weight costs an unpack, a
-// subtraction and M multiplies, with the warp-level tensor instruction (16 x 8 x 16, fp32 sums) about
-// 1.4 instructions for any M up to 8.  (tcgen05 would need the unpacked weights in shared or tensor
+// subtraction and M multiplies, with the warp-level tensor instruction (16 x 8 x 16, fp32 sums) the same
+// for any M up to 8.  (tcgen05 would need the unpacked weights in shared or tensor
 // memory first; here they stay in the registers that unpacked them.)  K order inside one instruction
 // is free as long as both operands agree, which makes the packed layout fit without any shuffle: a
 // thread's word of 8 codes (row n, columns k .. k + 7) is four pairs (i, i + 4) that mask out of the
-// word side by side, and its 16 bytes of X (token, k .. k + 7) are the matching pairs.  q - z is exact
-// in bf16 and fp16, P = X (q - z)^T is summed over a group and enters y as s P in fp32.
+// word side by side, and its 16 bytes of X (token, k .. k + 7) are the matching pairs.  Codes become
+// numbers by the published exponent-bias method: placed in the low fraction bits of a bf16 or fp16 power of
+// two they are that power plus the code, and one subtraction takes it and z away.  q - z is exact
+// in bf16 and fp16, P = X (q - z)^T is summed over a group (128 columns at most, as the tensor instruction
+// may cut its sums off) and enters y as s P in fp32.
 // A CTA owns 128 rows n and a run of columns.  One warp fills a ring of stages of 256 columns with TMA
 // (or bulk copies of rows), which keeps some 100 KB in flight on an SM and costs the others no issue
 // slots; four warps take 32 rows each of a stage's first 128 columns, four of the others.  The halves'
 // sums, and those of the CTAs of a cluster that split K, are joined in a fixed order through shared
 // memory.
 //
-// Measured, packed words from memory: 4-bit groups of 128, one token through 4096 x 4096 7.7 us (8.9 MB,
-// 1.1 TB/s: of that about 4.6 us are launch, first loads and the join), through 11008 x 4096 14.7 us; eight
-// e4m3 tokens through 50001 x 8192 (odd row count: bulk copies of rows) 101 us (214 MB, 2.1 TB/s); 16
-// tokens through 11008 x 4096, 3 bits, groups of 64, 31 us.  The copies alone would take a third of
-// that: the time is instruction issue and the fixed cost of a stage (a barrier to pass, scales, a flush
-// per group).
+// Measured, all inputs from memory: 4-bit groups of 128, one token through 4096 x 4096 8.6 us (8.9 MB,
+// 1.0 TB/s: of that about 4.6 us are launch, first loads and the join), through 11008 x 4096 15.6 us; eight
+// e4m3 tokens through 50001 x 8192 (odd row count: bulk copies of rows) 102 us (214 MB, 2.1 TB/s); 16
+// tokens through 11008 x 4096, 3 bits, groups of 64, 32 us.  The copies alone would take a third of
+// that.  By the counters of the 50001 x 8192 product 65 % of the issue slots are used, 5.1 instructions a
+// weight, of which unpacking, subtracting and multiplying are about 2; the rest (rows that start between
+// 16-byte boundaries, X widened by each of the warps, polling, a flush per group) is not separated.
 //
 // gemv_act_kernel (g_idx: any column in any group): see there.
 #pragma once
@@ -564,10 +568,11 @@ __global__ void __launch_bounds__(GM_THREADS, GmCfg<BITS, XT, MT, GROUPS>::CTAS)
 // significant bits) is formed in fp32 without rounding and cut into bf16 parts that hold it exactly (two
 // for codes of up to 4 bits, three for 8 bits), so the products are exact and the sums fp32, and a
 // weight's decoding and cutting, some 14 instructions, serve up to 32 tokens.
-// Bound by instruction issue: 4096 x 11008, 4-bit groups of 128, 2 tokens 38 us, 16 tokens 42 us, 64
-// tokens in two tiles 96 us.  fp32 multiply-adds in place of the tensor instruction took 39 us for 2
-// tokens and 119 us for 8.  Where the table does not fit (above 1280 groups), TABLE is false and every
-// weight's entry is read from global memory.
+// Bound by instruction issue: 4096 x 11008, 4-bit groups of 128, all inputs from memory, 2 or 8 tokens
+// 47 us, 16 tokens 51 us, 64 tokens in two tiles 106 us.  fp32 multiply-adds in place of the tensor
+// instruction took three times as long for 8 tokens.  Where the table does not fit (above 1280 groups), TABLE
+// is false and every weight's entry is read from global memory (4 tokens through 4096 x 32768, groups of
+// 16: 410 us).
 constexpr int GA_THREADS = 256, GA_ROWS = 32;
 constexpr int GA_TABLE = 160 * 1024;   // bytes of the table, at most
 

@@ -2,7 +2,7 @@
 // root-mean-square norm:
 //
 //   h = X (+ R),   v = h w  (v = h without a norm),   a = max_k |v_k|,
-//   r = 1 / sqrt(mean(h^2) + eps)  (r = 1 without a norm),
+//   r = 1 / sqrt(mean(h^2) + eps)  (r = 1 without a norm; the sum in fp32, see SquareSum for its range),
 //   x_scale = r a / 448,   X8 = e4m3(448 v / a),   R' = h rounded to R's type.
 //
 // r is positive and common to a row, so it scales a but cancels from the codes: one sum and one
@@ -10,8 +10,8 @@
 // whose order is that of the magnitudes with NaN above infinity, so a NaN reaches x_scale.
 //
 // Bound by memory for many rows: 2048 x 4096 bf16 with residual 12 us (58.7 MB, 4.9 TB/s; of it about
-// 2.5 us launch and tail), 8192 rows 37.6 us (6.2 TB/s), 4096 x 11008 bf16 without norm 24 us (5.7 TB/s),
-// 8191 x 16384 fp32 122 us (5.5 TB/s); by latency for few: 2.4 us for one row, 2.7 us for 64.  Long rows
+// 2.5 us launch and tail), 8192 rows 37.6 us (6.2 TB/s), 4096 x 11008 bf16 without norm 24 us (5.6 TB/s),
+// 8191 x 16384 fp32 123 us (5.5 TB/s); by latency for few: 2.4 us for one row, 2.7 us for 64.  Long rows
 // (512 x 65536 bf16 with residual) take 63 us; without the code for sums that fp32 does not hold, 57 us.
 #pragma once
 #include <cuda_bf16.h>
